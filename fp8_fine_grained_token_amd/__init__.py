@@ -16,3 +16,29 @@ from .binding import (  # noqa: F401
     fp8_fused_quant_kernel_workspace_bytes, fp8_quant_act_128x1_t_pow2,
     fp8_block_gemm_wgrad_pow2, fp8_block_gemm_dgrad_pow2,
 )
+
+_MOE = (
+    "FP8_W4_F32_1X128", "FP8_W4_E8M0_1X32", "fp8_moe_sort", "fp8_moe_sort_workspace_bytes",
+    "fp8_moe_dispatch", "fp8_moe_dispatch_quant_1x128", "fp8_moe_dispatch_quant_1x128_pow2",
+    "fp8_moe_sort_dispatch", "fp8_moe_sort_dispatch_quant_1x128",
+    "fp8_moe_sort_dispatch_quant_1x128_pow2", "fp8_moe_dispatch_grad", "fp8_moe_combine",
+    "fp8_moe_combine_grad", "fp8_norm_residual", "fp8_norm_residual_quant_1x128",
+    "fp8_norm_residual_quant_1x128_pow2", "fp8_norm_residual_grad",
+    "fp8_norm_residual_grad_workspace_bytes", "fp8_w4_quant_1x128", "fp8_w4_quant_1x32",
+    "fp8_w4_matvec", "fp8_w4_grouped_matvec",
+)
+
+
+def __getattr__(name):
+    """The operators around the expert products, from ``moe`` on first use
+    (it needs torch, which importing this package does not load)."""
+    if name in _MOE:
+        from . import moe
+        value = getattr(moe, name)
+        globals()[name] = value
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted(set(globals()) | set(_MOE))
