@@ -75,68 +75,320 @@ __global__ __launch_bounds__(256) void w4_quant_kernel(const uint16_t *__restric
 }
 
 // ---- products -----------------------------------------------------------------
+//
+// y = x w^T on the bf16 matrix cores: an E2M1 value times a power of two is a
+// bf16 number, a product of two bf16 numbers is exact in FP32, and the sums
+// are the matrix core's FP32 ones.  v_cvt_scalef32_pk_bf16_fp4 unpacks two
+// codes an instruction and applies the E8M0 scale on the way (half a lane
+// operation a weight, where the card's vector units have about three to
+// spare at the rate the weights arrive); an FP32 group scale multiplies the
+// group's 128-deep partial sum instead.
+//
+// A workgroup is eight waves.  A wave holds its part of x, up to kBlocks
+// 128-channel blocks of 16 rows, in registers for the whole call and streams
+// code rows past it, 16 bytes a lane: lane (c, q) of 16 x 4 reads channels
+// 32 q .. 32 q + 31 of a block of the row of column c, which is the operand
+// of four 16x16x32 products (each takes eight channels of every q, x alike).
+// `split` waves share a column tile along K and their sums meet in LDS.
+//
+// Few rows leave matrix columns unused, so kSegs of 1, 2 or 4 puts as many
+// stretches of K side by side: the 16 operand rows are then 16 / kSegs rows
+// of x in kSegs stretches, the 16 columns 16 / kSegs output columns in the
+// same stretches, and of the 16 x 16 products only those of equal stretches
+// are added up.  That makes tiles of 8 or 4 columns, for outputs too narrow
+// to fill the card with tiles of 16.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-    const uint32_t m = c & 7;
-    const float v = m < 2 ? 0.5f * (float)m : __uint_as_float(((m >> 1) + 126) << 23 | (m & 1) << 22);
-    return c & 8 ? -v : v;
+constexpr int kWaves = 8;
+constexpr int kBlockK = 128;  // channels of a block
+constexpr int kHeld = 8;      // blocks of 16 rows of x a wave holds
+
+struct W4Shape {
+    int64_t ldx, N, K;
+    int R, E;
+    int blocks;      // 128-channel blocks of a row, the last one perhaps in part
+    int split_log;   // log2 of the waves that share a column tile
+    int per;         // blocks of a stretch (<= kHeld / kSegs)
+    int chunks;      // passes over K of all stretches
+    int steps;       // column tiles of a wave
+};
+
+__device__ __forceinline__ bf16x8 weights8(uint32_t codes, float scale) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// One wave per output column, 16 rows of x at a time.
-constexpr int kRows = 16;
-
-template <bool kE8m0, typename Out>
-__global__ __launch_bounds__(256) void w4_matvec_kernel(
-    const Bf16 *__restrict__ x, int64_t ldx, const uint8_t *__restrict__ codes,
-    const void *__restrict__ scales, const int32_t *__restrict__ offsets, int64_t R, int64_t N,
-    int64_t K, Out *__restrict__ y) {
+// The `which`-th expert that has rows, its first row and the end of its rows
+// (r0 >= r1 where there are fewer): offsets clamped to [0, R], no range
+// starting before an earlier one ends.  A grid over the experts with rows
+// instead of all: one token sends 8 rows to 8 of 256 experts.
+__device__ __forceinline__ void busy_expert(const int32_t *offsets, int E, int R, int which,
+                                            int &e, int &r0, int &r1) {
     const int lane = threadIdx.x & 63;
-    const int64_t n = blockIdx.x * 4ll + (threadIdx.x >> 6);
-    if (n >= N) return;
-    const int64_t e = blockIdx.y;
-    int64_t r0 = 0, r1 = R;
-    if (offsets) {
-        // an expert's range starts no earlier than any before it ends
-        int64_t low = 0;
-        for (int64_t i = 0; i <= e; ++i) {
-            const int64_t o = offsets[i];
-            const int64_t c = o < 0 ? 0 : o > R ? R : o;
-            low = c > low ? c : low;
+    int low = 0, seen = 0;  // end of the ranges so far, experts with rows so far
+    e = r0 = r1 = 0;
+    for (int first = 0; first < E; first += 64) {
+        const int i = first + lane;
+        const int start = min(offsets[min(i, E)], R), stop = min(offsets[min(i + 1, E)], R);
+        int up = max(start, low);  // running maximum: where expert i's rows begin
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int v = __shfl_up(up, d);
+            if (lane >= d) up = max(up, v);
         }
-        const int64_t o = offsets[e + 1];
-        r0 = low;
-        r1 = o < low ? low : o > R ? R : o;
+        const uint64_t busy = __ballot(i < E && stop > up);
+        const int here = __popcll(busy);
+        if (which < seen + here) {
+            const uint64_t below = busy & ((1ull << lane) - 1);
+            const uint64_t mine =
+                __ballot(((busy >> lane) & 1) && __popcll(below) == which - seen);
+            const int src = __ffsll((unsigned long long)mine) - 1;
+            e = first + src;
+            r0 = __shfl(up, src);
+            r1 = __shfl(stop, src);
+            break;
+        }
+        seen += here;
+        low = max(__shfl(up, 63), low);
     }
-    const int64_t row_bytes = (K + 1) / 2, row = e * N + n;
-    const uint8_t *c = codes + row * row_bytes;
-    for (int64_t m0 = r0; m0 < r1; m0 += kRows) {
-        float acc[kRows] = {};
-        const int rows = r1 - m0 < kRows ? (int)(r1 - m0) : kRows;
-        for (int64_t b = lane; b < row_bytes; b += 64) {
-            const int64_t k = 2 * b;
-            float s;
+    e = __builtin_amdgcn_readfirstlane(e);
+    r0 = __builtin_amdgcn_readfirstlane(r0);
+    r1 = __builtin_amdgcn_readfirstlane(r1);
+}
+
+// The low 16 bytes of v moved down by `bytes` (0 to 16), zeros from above.
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, int bytes) {
+    uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
+    const int s = 8 * (bytes & 7);
+    const uint64_t low = lo >> s | hi << 1 << (63 - s), high = hi >> s;
+    lo = bytes < 8 ? low : bytes < 16 ? high : 0;
+    hi = bytes < 8 ? high : 0;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
+template <bool kE8m0, int kSegs, typename Out>
+__global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
+    const Bf16 *__restrict__ x, const uint8_t *__restrict__ codes,
+    const void *__restrict__ scales, const int32_t *__restrict__ offsets, W4Shape p,
+    Out *__restrict__ y) {
+    constexpr int kCols = 16 / kSegs;       // rows of x and output columns of a tile
+    constexpr int kBlocks = kHeld / kSegs;  // blocks of a stretch held at most
+    __shared__ float sums[2][kWaves][16][17];
+    __shared__ __attribute__((aligned(16))) uint16_t end_of_x[kCols][kBlockK];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int c = lane & 15, q = lane >> 4;
+    const int col = c % kCols, seg = c / kCols;
+    const int split = 1 << p.split_log, tiles_each = kWaves >> p.split_log;
+    const int along = wave & (split - 1), sub = wave >> p.split_log;
+    int e = 0, r0 = 0, r1 = p.R;
+    if (offsets) busy_expert(offsets, p.E, p.R, blockIdx.y, e, r0, r1);
+
+    const int64_t row_bytes = (p.K + 1) / 2, all_rows = p.E * p.N;
+    const int groups = kE8m0 ? (int)((p.K + 31) / 32) : p.blocks;
+    const int stretches = split * kSegs;
+    const int64_t tile0 = (int64_t)blockIdx.x * p.steps * tiles_each + sub;
+
+    const int full = (int)(p.K / kBlockK);  // whole blocks; one more, in part, if blocks > full
+
+    for (int m0 = r0; m0 < r1; m0 += kCols) {
+        const int rows = min(kCols, r1 - m0);
+        const Bf16 *xrow = x + (int64_t)(m0 + min(col, rows - 1)) * p.ldx;
+        bf16x8 held[kBlocks][4];
+        u32x4 code[kBlocks];
+        float scale[kBlocks];
+
+        // the first block of this lane's stretch in pass `chunk`
+        auto first_block = [&](int chunk) {
+            return (chunk * stretches + along * kSegs + seg) * p.per;
+        };
+        // x is zero past K: the block that K ends in is brought to LDS with
+        // its zeros, once for these rows.
+        if (p.blocks > full) {
+            for (int i = threadIdx.x; i < kCols * kBlockK; i += 64 * kWaves) {
+                const int m = i / kBlockK, k = i % kBlockK;
+                const int64_t at = (int64_t)full * kBlockK + k;
+                end_of_x[m][k] =
+                    m < rows && at < p.K ? x[(int64_t)(m0 + m) * p.ldx + at].bits : (uint16_t)0;
+            }
+            __syncthreads();
+        }
+        auto load_x = [&](int chunk) {
+            const int b0 = first_block(chunk);
+            const Bf16 *from = xrow + (int64_t)b0 * kBlockK + 32 * q;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                if (b >= p.per) continue;
+                u32x4 v[4] = {};
+                if (b0 + b < full) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = *reinterpret_cast<const u32x4_any *>(from + b * kBlockK + 8 * i);
+                }
+                if (p.blocks > full && b0 + b == full) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = *reinterpret_cast<const u32x4 *>(&end_of_x[col][32 * q + 8 * i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) held[b][i] = __builtin_bit_cast(bf16x8, v[i]);
+            }
+        };
+        // Where this lane's blocks of a tile begin and how many there are (x is
+        // zero in the others, whose codes and scales stay what they were).
+        // What is read past the end of a row meets zeros of x as well.  Only
+        // the last block of the last rows could reach past the end of all
+        // codes: there the 16 bytes begin `back` bytes earlier, to be moved
+        // down before they are used.
+        const uint8_t *from;
+        const void *scale_from;
+        int count, last, back, last_group;
+        auto place = [&](int64_t tile, int chunk) {
+            const int b0 = first_block(chunk);
+            int64_t n = tile * kCols + col;
+            n = n < p.N ? n : p.N - 1;  // a column past the end is not stored
+            const int64_t row = e * p.N + n;
+            const int64_t at = (int64_t)b0 * 64 + 16 * q;
+            from = codes + row * row_bytes + at;
+            count = min(p.blocks - b0, p.per);
+            last = p.blocks - 1 - b0;
+            const int64_t left = (all_rows - row) * row_bytes - at - 64 * (int64_t)last;
+            back = left < 16 ? 16 - (int)left : 0;
             if (kE8m0) {
-                const int E = static_cast<const uint8_t *>(scales)[row * ((K + 31) / 32) + k / 32];
-                s = ldexpf(1.0f, E - 127);
+                const int g = 4 * b0 + q;
+                scale_from = static_cast<const uint8_t *>(scales) + row * groups + g;
+                last_group = groups - 1 - g;
             } else {
-                s = static_cast<const float *>(scales)[row * ((K + 127) / 128) + k / 128];
+                scale_from = static_cast<const float *>(scales) + row * groups + b0;
             }
-            const uint32_t pair = c[b];
-            const float w0 = s * e2m1_value(pair & 15);
-            const float w1 = k + 1 < K ? s * e2m1_value(pair >> 4) : 0.0f;
+        };
+        auto load_weights = [&](int b) {
+            if (b >= count) return;
+            code[b] =
+                *reinterpret_cast<const u32x4_any *>(from + (64 * b - (b == last ? back : 0)));
+            if (kE8m0)
+                scale[b] = __uint_as_float(
+                    (uint32_t)static_cast<const uint8_t *>(scale_from)[min(4 * b, last_group)]
+                    << 23);
+            else
+                scale[b] = static_cast<const float *>(scale_from)[b];
+        };
+
+        const int64_t units = (int64_t)p.steps * p.chunks;
+        load_x(0);
+        place(tile0, 0);
 #pragma unroll
-            for (int m = 0; m < kRows; ++m) {
-                if (m >= rows) continue;
-                const Bf16 *p = x + (m0 + m) * ldx + k;
-                acc[m] = __builtin_fmaf(to_float(p[0]), w0, acc[m]);
-                if (k + 1 < K) acc[m] = __builtin_fmaf(to_float(p[1]), w1, acc[m]);
+        for (int b = 0; b < kBlocks; ++b) {
+            code[b] = u32x4{0, 0, 0, 0};
+            scale[b] = 0.0f;
+            load_weights(b);
+        }
+        f32x4 acc = {0, 0, 0, 0};
+        int buffer = 0, chunk = 0;
+        int64_t tile = tile0;
+        for (int64_t u = 0; u < units; ++u) {
+            // the unit after this one: its codes are asked for as soon as the
+            // present ones are unpacked
+            const bool more = u + 1 < units;
+            const int next_chunk = chunk + 1 < p.chunks ? chunk + 1 : 0;
+            const int64_t next_tile = next_chunk ? tile : tile + tiles_each;
+            const int cut = back > 0 ? last : -1, cut_back = min(back, 16);
+            if (more) place(next_tile, next_chunk);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                if (b >= p.per) continue;
+                if (__any(b == cut)) {
+                    const u32x4 moved = shift_down(code[b], cut_back);
+                    if (b == cut) code[b] = moved;
+                }
+                bf16x8 w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = weights8(code[b][i], kE8m0 ? scale[b] : 1.0f);
+                const float s = scale[b];
+                if (more) load_weights(b);
+                if (kE8m0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(held[b][i], w[i], acc, 0, 0,
+                                                                      0);
+                } else {
+                    f32x4 part = {0, 0, 0, 0};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(held[b][i], w[i], part, 0,
+                                                                       0, 0);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(s, part[r], acc[r]);
+                }
             }
-        }
+            if (p.chunks > 1 && more) load_x(next_chunk);
+            if (next_chunk == 0) {
+                // element (4 q + r, c) of the product: x row, output column
+                float(*mine)[17] = sums[buffer][wave];
 #pragma unroll
-        for (int m = 0; m < kRows; ++m) {
-            for (int d = 32; d; d /= 2) acc[m] += __shfl_xor(acc[m], d);
-            if (m < rows && lane == 0) from_float(acc[m], y[(m0 + m) * N + n]);
+                for (int r = 0; r < 4; ++r) mine[4 * q + r][c] = acc[r];
+                __syncthreads();
+                const int64_t first = tile - sub;
+                for (int o = threadIdx.x; o < tiles_each * rows * kCols; o += 64 * kWaves) {
+                    const int which = o / (rows * kCols);
+                    const int m = o / kCols % rows, n = o % kCols;
+                    const int64_t at = (first + which) * kCols + n;
+                    if (at >= p.N) continue;
+                    float sum = 0;
+                    for (int w = 0; w < split; ++w)
+#pragma unroll
+                        for (int g = 0; g < kSegs; ++g)
+                            sum += sums[buffer][which * split + w][m + g * kCols][n + g * kCols];
+                    from_float(sum, y[(int64_t)(m0 + m) * p.N + at]);
+                }
+                buffer ^= 1;
+                acc = f32x4{0, 0, 0, 0};
+            }
+            chunk = next_chunk;
+            tile = next_tile;
         }
+        __syncthreads();  // the next rows begin with the first buffer again
+    }
+}
+
+// Codes of fewer than 16 bytes in all: the kernel above reads 16 at a time.
+// One thread a sum of at most 30 products.
+template <bool kE8m0, typename Out>
+__global__ __launch_bounds__(256) void w4_few_codes_kernel(
+    const Bf16 *__restrict__ x, const uint8_t *__restrict__ codes,
+    const void *__restrict__ scales, const int32_t *__restrict__ offsets, W4Shape p,
+    Out *__restrict__ y) {
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < p.R * p.N; i += gridDim.x * 256ll) {
+        const int64_t m = i / p.N;
+        int64_t row = i % p.N;
+        if (offsets) {
+            int e = 0, low = min(max(offsets[0], 0), p.R);  // the end of the ranges so far
+            if (m < low) continue;
+            for (; e < p.E; ++e) {
+                low = max(low, min(offsets[e + 1], p.R));
+                if (m < low) break;
+            }
+            if (e == p.E) continue;
+            row += e * p.N;
+        }
+        float sum = 0;
+        for (int64_t k = 0; k < p.K; ++k) {
+            const uint32_t code = codes[row * ((p.K + 1) / 2) + k / 2] >> (4 * (k & 1));
+            const float s = kE8m0 ? __uint_as_float((uint32_t)static_cast<const uint8_t *>(
+                                                        scales)[row * ((p.K + 31) / 32) + k / 32]
+                                                    << 23)
+                                  : static_cast<const float *>(scales)[row];
+            const bf16x2 w =
+                __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code & 15, kE8m0 ? s : 1.0f, 0);
+            const float value = kE8m0 ? (float)w[0] : s * (float)w[0];
+            sum = __builtin_fmaf(to_float(x[m * p.ldx + k]), value, sum);
+        }
+        from_float(sum, y[i]);
     }
 }
 
@@ -155,17 +407,65 @@ hipError_t launch_w4_quant(const void *w, int64_t N, int64_t K, void *codes, voi
 hipError_t launch_w4_matvec(const void *x, int64_t ldx, const void *codes, const void *scales,
                             bool e8m0, const int32_t *offsets, int64_t E, int64_t R, int64_t N,
                             int64_t K, void *y, bool bf16_out, hipStream_t stream) {
-    const dim3 grid((unsigned)((N + 3) / 4), (unsigned)E);
+    W4Shape p;
+    p.ldx = ldx;
+    p.N = N;
+    p.K = K;
+    p.R = (int)R;
+    p.E = (int)E;
+    p.blocks = (int)((K + kBlockK - 1) / kBlockK);
+    // Workgroups that can be busy: experts with rows times column tiles.
+    // Stretches of K side by side (kSegs) and waves along K (split) both make
+    // more and narrower tiles; they are taken as far as the card needs them.
+    const int64_t active = offsets ? (E < R ? E : R) : 1;
+    const int64_t want = 256;
+    int segs = 1, split_log = 0;
+    while ((1 << split_log) * kHeld < p.blocks && (1 << split_log) < kWaves) ++split_log;
+    auto groups = [&] {
+        const int64_t tiles = (N + 16 / segs - 1) / (16 / segs), each = kWaves >> split_log;
+        return (tiles + each - 1) / each * active;
+    };
+    while (groups() < want && (1 << split_log) < kWaves && (1 << split_log) < p.blocks)
+        ++split_log;
+    while (groups() < want && segs < 4 && R <= 16 / (2 * segs) &&
+           (segs << split_log) < p.blocks)
+        segs *= 2;
+    const int64_t stretches = (int64_t)segs << split_log;
+    p.split_log = split_log;
+    p.per = (int)((p.blocks + stretches - 1) / stretches);
+    if (p.per < 1) p.per = 1;  // K = 0: no block, zeros
+    if (p.per > kHeld / segs) p.per = kHeld / segs;
+    p.chunks = (int)((p.blocks + stretches * p.per - 1) / (stretches * p.per));
+    if (p.chunks < 1) p.chunks = 1;
+    const int64_t total = groups() / active;  // workgroups of an expert at one step each
+    p.steps = 1;
+    const int64_t target = offsets ? 1024 : 512;
+    if (total * active > target) p.steps = (int)((total * active + target - 1) / target);
+    const dim3 grid((unsigned)((total + p.steps - 1) / p.steps), (unsigned)active);
+    const bool few = E * N * ((K + 1) / 2) < 16 && K > 0;
     auto go = [&](auto out, auto *kernel) {
         using Out = decltype(out);
-        kernel<<<grid, 256, 0, stream>>>(static_cast<const Bf16 *>(x), ldx,
-                                         static_cast<const uint8_t *>(codes), scales, offsets, R,
-                                         N, K, static_cast<Out *>(y));
+        if (few)
+            kernel = e8m0 ? w4_few_codes_kernel<true, Out> : w4_few_codes_kernel<false, Out>;
+        const int64_t sums = R * N < (1 << 22) ? R * N : (1 << 22);
+        kernel<<<few ? dim3((unsigned)((sums + 255) / 256)) : grid, few ? 256 : 64 * kWaves, 0,
+                 stream>>>(static_cast<const Bf16 *>(x),
+                                                 static_cast<const uint8_t *>(codes), scales,
+                                                 offsets, p, static_cast<Out *>(y));
     };
-    if (bf16_out)
-        go(Bf16{}, e8m0 ? w4_matvec_kernel<true, Bf16> : w4_matvec_kernel<false, Bf16>);
-    else
-        go(float{}, e8m0 ? w4_matvec_kernel<true, float> : w4_matvec_kernel<false, float>);
+    auto typed = [&](auto out) {
+        using Out = decltype(out);
+        if (e8m0) {
+            go(out, segs == 1   ? w4_matvec_kernel<true, 1, Out>
+                    : segs == 2 ? w4_matvec_kernel<true, 2, Out>
+                                : w4_matvec_kernel<true, 4, Out>);
+        } else {
+            go(out, segs == 1   ? w4_matvec_kernel<false, 1, Out>
+                    : segs == 2 ? w4_matvec_kernel<false, 2, Out>
+                                : w4_matvec_kernel<false, 4, Out>);
+        }
+    };
+    if (bf16_out) typed(Bf16{}); else typed(float{});
     return hipGetLastError();
 }
 
