@@ -7,6 +7,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "launch_moe.hpp"
 #include "vec.hpp"
@@ -84,12 +86,14 @@ __global__ __launch_bounds__(256) void w4_quant_kernel(const uint16_t *__restric
 // spare at the rate the weights arrive); an FP32 group scale multiplies the
 // group's 128-deep partial sum instead.
 //
-// A workgroup is eight waves.  A wave holds its part of x, up to kBlocks
-// 128-channel blocks of 16 rows, in registers for the whole call and streams
-// code rows past it, 16 bytes a lane: lane (c, q) of 16 x 4 reads channels
-// 32 q .. 32 q + 31 of a block of the row of column c, which is the operand
-// of four 16x16x32 products (each takes eight channels of every q, x alike).
-// `split` waves share a column tile along K and their sums meet in LDS.
+// A workgroup is eight waves.  A wave holds its part of x, kPer 128-channel
+// blocks of 16 rows, in registers for the whole call and streams code rows
+// past it, 16 bytes a lane: lane (c, q) of 16 x 4 reads channels 32 q ..
+// 32 q + 31 of a block of the row of column c, which is the operand of four
+// 16x16x32 products (each takes eight channels of every q, x alike).  The
+// codes of the next tile are asked for, into the registers of the present
+// ones, as soon as these are unpacked.  `split` waves share a column tile
+// along K and their sums meet in LDS.
 //
 // Few rows leave matrix columns unused, so kSegs of 1, 2 or 4 puts as many
 // stretches of K side by side: the 16 operand rows are then 16 / kSegs rows
@@ -111,9 +115,9 @@ struct W4Shape {
     int R, E;
     int blocks;      // 128-channel blocks of a row, the last one perhaps in part
     int split_log;   // log2 of the waves that share a column tile
-    int per;         // blocks of a stretch (<= kHeld / kSegs)
     int chunks;      // passes over K of all stretches
     int steps;       // column tiles of a wave
+    bool bf16_out;
 };
 
 __device__ __forceinline__ bf16x8 weights8(uint32_t codes, float scale) {
@@ -172,13 +176,12 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 v, int bytes) {
     return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
-template <bool kE8m0, int kSegs, typename Out>
+template <bool kE8m0, int kSegs, int kPer, bool kChunked>
 __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
     const Bf16 *__restrict__ x, const uint8_t *__restrict__ codes,
     const void *__restrict__ scales, const int32_t *__restrict__ offsets, W4Shape p,
-    Out *__restrict__ y) {
-    constexpr int kCols = 16 / kSegs;       // rows of x and output columns of a tile
-    constexpr int kBlocks = kHeld / kSegs;  // blocks of a stretch held at most
+    void *__restrict__ y) {
+    constexpr int kCols = 16 / kSegs;  // rows of x and output columns of a tile
     __shared__ float sums[2][kWaves][16][17];
     __shared__ __attribute__((aligned(16))) uint16_t end_of_x[kCols][kBlockK];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -193,19 +196,18 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
     const int groups = kE8m0 ? (int)((p.K + 31) / 32) : p.blocks;
     const int stretches = split * kSegs;
     const int64_t tile0 = (int64_t)blockIdx.x * p.steps * tiles_each + sub;
-
     const int full = (int)(p.K / kBlockK);  // whole blocks; one more, in part, if blocks > full
 
     for (int m0 = r0; m0 < r1; m0 += kCols) {
         const int rows = min(kCols, r1 - m0);
         const Bf16 *xrow = x + (int64_t)(m0 + min(col, rows - 1)) * p.ldx;
-        bf16x8 held[kBlocks][4];
-        u32x4 code[kBlocks];
-        float scale[kBlocks];
+        bf16x8 held[kPer][4];
+        u32x4 code[kPer];
+        uint32_t scale[kPer];  // as loaded: E8M0 byte or FP32 bits
 
         // the first block of this lane's stretch in pass `chunk`
         auto first_block = [&](int chunk) {
-            return (chunk * stretches + along * kSegs + seg) * p.per;
+            return (chunk * stretches + along * kSegs + seg) * kPer;
         };
         // x is zero past K: the block that K ends in is brought to LDS with
         // its zeros, once for these rows.
@@ -218,14 +220,15 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
             }
             __syncthreads();
         }
+        // Lanes of rows past the last stay zero and idle: with one row the
+        // loads touch a sixteenth of the lanes.
         auto load_x = [&](int chunk) {
             const int b0 = first_block(chunk);
             const Bf16 *from = xrow + (int64_t)b0 * kBlockK + 32 * q;
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                if (b >= p.per) continue;
+            for (int b = 0; b < kPer; ++b) {
                 u32x4 v[4] = {};
-                if (b0 + b < full) {
+                if (b0 + b < full && col < rows) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         v[i] = *reinterpret_cast<const u32x4_any *>(from + b * kBlockK + 8 * i);
@@ -239,15 +242,14 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
                 for (int i = 0; i < 4; ++i) held[b][i] = __builtin_bit_cast(bf16x8, v[i]);
             }
         };
-        // Where this lane's blocks of a tile begin and how many there are (x is
-        // zero in the others, whose codes and scales stay what they were).
-        // What is read past the end of a row meets zeros of x as well.  Only
-        // the last block of the last rows could reach past the end of all
-        // codes: there the 16 bytes begin `back` bytes earlier, to be moved
-        // down before they are used.
+        // Where this lane's blocks of a tile begin.  Blocks past the row's last
+        // one read that again (x is zero there); what lies past the end of a
+        // row meets zeros of x as well.  Only the last block of the last rows
+        // could reach past the end of all codes: there the 16 bytes begin
+        // `back` bytes earlier, to be moved down before they are used.
         const uint8_t *from;
         const void *scale_from;
-        int count, last, back, last_group;
+        int end, back, last, last_group;
         auto place = [&](int64_t tile, int chunk) {
             const int b0 = first_block(chunk);
             int64_t n = tile * kCols + col;
@@ -255,10 +257,10 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
             const int64_t row = e * p.N + n;
             const int64_t at = (int64_t)b0 * 64 + 16 * q;
             from = codes + row * row_bytes + at;
-            count = min(p.blocks - b0, p.per);
             last = p.blocks - 1 - b0;
             const int64_t left = (all_rows - row) * row_bytes - at - 64 * (int64_t)last;
             back = left < 16 ? 16 - (int)left : 0;
+            end = 64 * last - back;
             if (kE8m0) {
                 const int g = 4 * b0 + q;
                 scale_from = static_cast<const uint8_t *>(scales) + row * groups + g;
@@ -268,49 +270,31 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
             }
         };
         auto load_weights = [&](int b) {
-            if (b >= count) return;
-            code[b] =
-                *reinterpret_cast<const u32x4_any *>(from + (64 * b - (b == last ? back : 0)));
+            code[b] = *reinterpret_cast<const u32x4_any *>(from + min(64 * b, end));
             if (kE8m0)
-                scale[b] = __uint_as_float(
-                    (uint32_t)static_cast<const uint8_t *>(scale_from)[min(4 * b, last_group)]
-                    << 23);
+                scale[b] = static_cast<const uint8_t *>(scale_from)[min(4 * b, last_group)];
             else
-                scale[b] = static_cast<const float *>(scale_from)[b];
+                scale[b] = static_cast<const uint32_t *>(scale_from)[min(b, last)];
         };
 
-        const int64_t units = (int64_t)p.steps * p.chunks;
-        load_x(0);
-        place(tile0, 0);
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            code[b] = u32x4{0, 0, 0, 0};
-            scale[b] = 0.0f;
-            load_weights(b);
-        }
         f32x4 acc = {0, 0, 0, 0};
-        int buffer = 0, chunk = 0;
-        int64_t tile = tile0;
-        for (int64_t u = 0; u < units; ++u) {
-            // the unit after this one: its codes are asked for as soon as the
-            // present ones are unpacked
-            const bool more = u + 1 < units;
-            const int next_chunk = chunk + 1 < p.chunks ? chunk + 1 : 0;
-            const int64_t next_tile = next_chunk ? tile : tile + tiles_each;
-            const int cut = back > 0 ? last : -1, cut_back = min(back, 16);
-            if (more) place(next_tile, next_chunk);
+        int buffer = 0;
+        // One tile (of one pass): unpack, ask for the next one's codes, add up.
+        auto products = [&](int cut, int cut_back, auto more) {
+            if (__any(cut >= 0 && cut < kPer)) {
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                if (b >= p.per) continue;
-                if (__any(b == cut)) {
-                    const u32x4 moved = shift_down(code[b], cut_back);
-                    if (b == cut) code[b] = moved;
-                }
+                for (int b = 0; b < kPer; ++b)
+                    if (b == cut) code[b] = shift_down(code[b], cut_back);
+            }
+#pragma unroll
+            for (int b = 0; b < kPer; ++b) {
+                const float s = __uint_as_float(kE8m0 ? scale[b] << 23 : scale[b]);
                 bf16x8 w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = weights8(code[b][i], kE8m0 ? scale[b] : 1.0f);
-                const float s = scale[b];
-                if (more) load_weights(b);
+                for (int i = 0; i < 4; ++i) w[i] = weights8(code[b][i], kE8m0 ? s : 1.0f);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (decltype(more)::value) load_weights(b);
+                __builtin_amdgcn_sched_barrier(0);
                 if (kE8m0) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -326,43 +310,62 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
                     for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(s, part[r], acc[r]);
                 }
             }
-            if (p.chunks > 1 && more) load_x(next_chunk);
-            if (next_chunk == 0) {
-                // element (4 q + r, c) of the product: x row, output column
-                float(*mine)[17] = sums[buffer][wave];
+        };
+        auto store = [&](int64_t tile) {
+            // element (4 q + r, c) of the product: x row, output column
+            float(*mine)[17] = sums[buffer][wave];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) mine[4 * q + r][c] = acc[r];
-                __syncthreads();
-                const int64_t first = tile - sub;
-                for (int o = threadIdx.x; o < tiles_each * rows * kCols; o += 64 * kWaves) {
-                    const int which = o / (rows * kCols);
-                    const int m = o / kCols % rows, n = o % kCols;
-                    const int64_t at = (first + which) * kCols + n;
-                    if (at >= p.N) continue;
-                    float sum = 0;
-                    for (int w = 0; w < split; ++w)
+            for (int r = 0; r < 4; ++r) mine[4 * q + r][c] = acc[r];
+            __syncthreads();
+            const int64_t first = tile - sub;
+            for (int o = threadIdx.x; o < tiles_each * rows * kCols; o += 64 * kWaves) {
+                const int which = o / (rows * kCols);
+                const int m = o / kCols % rows, n = o % kCols;
+                const int64_t at = (first + which) * kCols + n;
+                if (at >= p.N) continue;
+                float sum = 0;
+                for (int w = 0; w < split; ++w)
 #pragma unroll
-                        for (int g = 0; g < kSegs; ++g)
-                            sum += sums[buffer][which * split + w][m + g * kCols][n + g * kCols];
-                    from_float(sum, y[(int64_t)(m0 + m) * p.N + at]);
-                }
-                buffer ^= 1;
-                acc = f32x4{0, 0, 0, 0};
+                    for (int g = 0; g < kSegs; ++g)
+                        sum += sums[buffer][which * split + w][m + g * kCols][n + g * kCols];
+                const int64_t to = (int64_t)(m0 + m) * p.N + at;
+                if (p.bf16_out) from_float(sum, static_cast<Bf16 *>(y)[to]);
+                else static_cast<float *>(y)[to] = sum;
             }
-            chunk = next_chunk;
-            tile = next_tile;
+            buffer ^= 1;
+            acc = f32x4{0, 0, 0, 0};
+        };
+
+        place(tile0, 0);
+#pragma unroll
+        for (int b = 0; b < kPer; ++b) load_weights(b);
+        load_x(0);
+        const int64_t units = (int64_t)p.steps * p.chunks;
+        int chunk = 0;
+        int64_t tile = tile0;
+        for (int64_t u = 1; u < units; ++u) {
+            const int cut = back > 0 ? last : -1, cut_back = min(back, 16);
+            const int64_t done = tile;
+            if (kChunked) chunk = chunk + 1 < p.chunks ? chunk + 1 : 0;
+            if (!kChunked || chunk == 0) tile += tiles_each;
+            place(tile, chunk);
+            products(cut, cut_back, std::true_type{});
+            if (kChunked) load_x(chunk);
+            if (!kChunked || chunk == 0) store(done);
         }
+        products(back > 0 ? last : -1, min(back, 16), std::false_type{});
+        store(tile);
         __syncthreads();  // the next rows begin with the first buffer again
     }
 }
 
-// Codes of fewer than 16 bytes in all: the kernel above reads 16 at a time.
-// One thread a sum of at most 30 products.
-template <bool kE8m0, typename Out>
+// Codes of fewer than 16 bytes in all (or none): the kernel above reads 16 at
+// a time.  One thread a sum of at most 30 products.
+template <bool kE8m0>
 __global__ __launch_bounds__(256) void w4_few_codes_kernel(
     const Bf16 *__restrict__ x, const uint8_t *__restrict__ codes,
     const void *__restrict__ scales, const int32_t *__restrict__ offsets, W4Shape p,
-    Out *__restrict__ y) {
+    void *__restrict__ y) {
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < p.R * p.N; i += gridDim.x * 256ll) {
         const int64_t m = i / p.N;
         int64_t row = i % p.N;
@@ -388,8 +391,33 @@ __global__ __launch_bounds__(256) void w4_few_codes_kernel(
             const float value = kE8m0 ? (float)w[0] : s * (float)w[0];
             sum = __builtin_fmaf(to_float(x[m * p.ldx + k]), value, sum);
         }
-        from_float(sum, y[i]);
+        if (p.bf16_out) from_float(sum, static_cast<Bf16 *>(y)[i]);
+        else static_cast<float *>(y)[i] = sum;
     }
+}
+
+// The kernel for `segs` stretches side by side of `per` blocks each (rounded
+// up to one that is built; the blocks too many are read twice, times zero).
+using MatvecKernel = void (*)(const Bf16 *, const uint8_t *, const void *, const int32_t *,
+                              W4Shape, void *);
+template <bool kE8m0>
+MatvecKernel matvec_kernel(int segs, int &per, bool chunked) {
+    if (chunked) return w4_matvec_kernel<kE8m0, 1, 8, true>;
+    if (segs == 1) {
+        if (per <= 1) return per = 1, w4_matvec_kernel<kE8m0, 1, 1, false>;
+        if (per <= 2) return per = 2, w4_matvec_kernel<kE8m0, 1, 2, false>;
+        if (per <= 4) return per = 4, w4_matvec_kernel<kE8m0, 1, 4, false>;
+        if (per <= 6) return per = 6, w4_matvec_kernel<kE8m0, 1, 6, false>;
+        if (per <= 7) return per = 7, w4_matvec_kernel<kE8m0, 1, 7, false>;
+        return per = 8, w4_matvec_kernel<kE8m0, 1, 8, false>;
+    }
+    if (segs == 2) {
+        if (per <= 1) return per = 1, w4_matvec_kernel<kE8m0, 2, 1, false>;
+        if (per <= 2) return per = 2, w4_matvec_kernel<kE8m0, 2, 2, false>;
+        return per = 4, w4_matvec_kernel<kE8m0, 2, 4, false>;
+    }
+    if (per <= 1) return per = 1, w4_matvec_kernel<kE8m0, 4, 1, false>;
+    return per = 2, w4_matvec_kernel<kE8m0, 4, 2, false>;
 }
 
 }  // namespace
@@ -414,6 +442,16 @@ hipError_t launch_w4_matvec(const void *x, int64_t ldx, const void *codes, const
     p.R = (int)R;
     p.E = (int)E;
     p.blocks = (int)((K + kBlockK - 1) / kBlockK);
+    p.bf16_out = bf16_out;
+    const Bf16 *rows = static_cast<const Bf16 *>(x);
+    const uint8_t *bytes = static_cast<const uint8_t *>(codes);
+    if (K == 0 || E * N * ((K + 1) / 2) < 16) {
+        const int64_t sums = R * N < (1 << 22) ? R * N : (1 << 22);
+        auto *kernel = e8m0 ? w4_few_codes_kernel<true> : w4_few_codes_kernel<false>;
+        kernel<<<(unsigned)((sums + 255) / 256), 256, 0, stream>>>(rows, bytes, scales, offsets, p,
+                                                                   y);
+        return hipGetLastError();
+    }
     // Workgroups that can be busy: experts with rows times column tiles.
     // Stretches of K side by side (kSegs) and waves along K (split) both make
     // more and narrower tiles; they are taken as far as the card needs them.
@@ -421,51 +459,28 @@ hipError_t launch_w4_matvec(const void *x, int64_t ldx, const void *codes, const
     const int64_t want = 256;
     int segs = 1, split_log = 0;
     while ((1 << split_log) * kHeld < p.blocks && (1 << split_log) < kWaves) ++split_log;
+    const bool chunked = p.blocks > kHeld * kWaves;
     auto groups = [&] {
         const int64_t tiles = (N + 16 / segs - 1) / (16 / segs), each = kWaves >> split_log;
         return (tiles + each - 1) / each * active;
     };
     while (groups() < want && (1 << split_log) < kWaves && (1 << split_log) < p.blocks)
         ++split_log;
-    while (groups() < want && segs < 4 && R <= 16 / (2 * segs) &&
+    while (!chunked && groups() < want && segs < 4 && R <= 16 / (2 * segs) &&
            (segs << split_log) < p.blocks)
         segs *= 2;
-    const int64_t stretches = (int64_t)segs << split_log;
+    const int stretches = segs << split_log;
     p.split_log = split_log;
-    p.per = (int)((p.blocks + stretches - 1) / stretches);
-    if (p.per < 1) p.per = 1;  // K = 0: no block, zeros
-    if (p.per > kHeld / segs) p.per = kHeld / segs;
-    p.chunks = (int)((p.blocks + stretches * p.per - 1) / (stretches * p.per));
-    if (p.chunks < 1) p.chunks = 1;
+    int per = chunked ? kHeld : (p.blocks + stretches - 1) / stretches;
+    const MatvecKernel kernel =
+        e8m0 ? matvec_kernel<true>(segs, per, chunked) : matvec_kernel<false>(segs, per, chunked);
+    p.chunks = (p.blocks + stretches * per - 1) / (stretches * per);
     const int64_t total = groups() / active;  // workgroups of an expert at one step each
     p.steps = 1;
     const int64_t target = offsets ? 1024 : 512;
     if (total * active > target) p.steps = (int)((total * active + target - 1) / target);
     const dim3 grid((unsigned)((total + p.steps - 1) / p.steps), (unsigned)active);
-    const bool few = E * N * ((K + 1) / 2) < 16 && K > 0;
-    auto go = [&](auto out, auto *kernel) {
-        using Out = decltype(out);
-        if (few)
-            kernel = e8m0 ? w4_few_codes_kernel<true, Out> : w4_few_codes_kernel<false, Out>;
-        const int64_t sums = R * N < (1 << 22) ? R * N : (1 << 22);
-        kernel<<<few ? dim3((unsigned)((sums + 255) / 256)) : grid, few ? 256 : 64 * kWaves, 0,
-                 stream>>>(static_cast<const Bf16 *>(x),
-                                                 static_cast<const uint8_t *>(codes), scales,
-                                                 offsets, p, static_cast<Out *>(y));
-    };
-    auto typed = [&](auto out) {
-        using Out = decltype(out);
-        if (e8m0) {
-            go(out, segs == 1   ? w4_matvec_kernel<true, 1, Out>
-                    : segs == 2 ? w4_matvec_kernel<true, 2, Out>
-                                : w4_matvec_kernel<true, 4, Out>);
-        } else {
-            go(out, segs == 1   ? w4_matvec_kernel<false, 1, Out>
-                    : segs == 2 ? w4_matvec_kernel<false, 2, Out>
-                                : w4_matvec_kernel<false, 4, Out>);
-        }
-    };
-    if (bf16_out) typed(Bf16{}); else typed(float{});
+    kernel<<<grid, 64 * kWaves, 0, stream>>>(rows, bytes, scales, offsets, p, y);
     return hipGetLastError();
 }
 
