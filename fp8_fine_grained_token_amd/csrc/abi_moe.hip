@@ -21,6 +21,7 @@ inline void clear_last_error() { (void)hipGetLastError(); }
 
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
+constexpr int64_t kMaxInner = (int64_t)1 << 24;  // inner dimension of a 4-bit product
 
 inline bool dim_ok(int64_t n) { return n >= 0 && n < kMaxDim; }
 inline bool matrix_ok(int64_t rows, int64_t cols) {
@@ -169,7 +170,9 @@ fp8_status w4_matvec(const void *x, int64_t ldx, const void *codes, const void *
                      int64_t K, void *y, int out_dtype, void *stream) {
     if (!type_ok(out_dtype)) return FP8_ERR_DTYPE;
     if (kind != FP8_W4_F32_1X128 && kind != FP8_W4_E8M0_1X32) return FP8_ERR_DTYPE;
-    if (!matrix_ok(R, K) || !matrix_ok(R, N) || !matrix_ok(N, K)) return FP8_ERR_SHAPE;
+    // a tile's 16 rows of codes are addressed with 32-bit offsets
+    if (!matrix_ok(R, K) || !matrix_ok(R, N) || !matrix_ok(N, K) || K >= kMaxInner)
+        return FP8_ERR_SHAPE;
     if (!stride_ok(R, ldx)) return FP8_ERR_SHAPE;
     if (E < 0 || E > 65535 || N * K >= kMaxElems / (E > 0 ? E : 1)) return FP8_ERR_SHAPE;
     // a launch holds below 2^32 threads

@@ -87,13 +87,18 @@ __global__ __launch_bounds__(256) void w4_quant_kernel(const uint16_t *__restric
 // group's 128-deep partial sum instead.
 //
 // A workgroup is eight waves.  A wave holds its part of x, kPer 128-channel
-// blocks of 16 rows, in registers for the whole call and streams code rows
-// past it, 16 bytes a lane: lane (c, q) of 16 x 4 reads channels 32 q ..
-// 32 q + 31 of a block of the row of column c, which is the operand of four
-// 16x16x32 products (each takes eight channels of every q, x alike).  The
-// codes of the next tile are asked for, into the registers of the present
-// ones, as soon as these are unpacked.  `split` waves share a column tile
-// along K and their sums meet in LDS.
+// blocks of 16 rows, in registers for the whole call and streams tiles of 16
+// code rows (a stretch of 64 kPer bytes each) past it.  `split` waves share a
+// column tile along K and their sums meet in LDS.
+//
+// A tile's bytes are read with neighbouring lanes on neighbouring addresses
+// and brought into operand order by a trip through the wave's own part of
+// LDS: lane (c, q) of 16 x 4 takes channels 32 q .. 32 q + 31 of a block of
+// row c, the operand of four 16x16x32 products (each takes eight channels of
+// every q, x alike).  Read in operand order, every lane would touch a cache
+// line of its own and the 64 look-ups of a load, not HBM, were the bound (128
+// rows over 32 experts of 4096 x 7168: 131 us).  The next tile's loads are
+// under way while a tile is multiplied.
 //
 // Few rows leave matrix columns unused, so kSegs of 1, 2 or 4 puts as many
 // stretches of K side by side: the 16 operand rows are then 16 / kSegs rows
@@ -166,7 +171,7 @@ __device__ __forceinline__ void busy_expert(const int32_t *offsets, int E, int R
     r1 = __builtin_amdgcn_readfirstlane(r1);
 }
 
-// The low 16 bytes of v moved down by `bytes` (0 to 16), zeros from above.
+// v moved down by `bytes` (0 to 16), zeros from above.
 __device__ __forceinline__ u32x4 shift_down(u32x4 v, int bytes) {
     uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
     const int s = 8 * (bytes & 7);
@@ -176,43 +181,144 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 v, int bytes) {
     return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
+// What a wave has written to its own LDS is read by its other lanes: the
+// LDS keeps a wave's order, the compiler has to as well.
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// How far before `at` a read of kBytes has to begin to end with the array,
+// `left` bytes from `at` (0 where it ends inside).
+template <int kBytes>
+__device__ __forceinline__ int end_back(int64_t left) {
+    return left >= kBytes ? 0 : (int)(kBytes - left);
+}
+
 template <bool kE8m0, int kSegs, int kPer, bool kChunked>
 __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
     const Bf16 *__restrict__ x, const uint8_t *__restrict__ codes,
-    const void *__restrict__ scales, const int32_t *__restrict__ offsets, W4Shape p,
+    const uint8_t *__restrict__ scales, const int32_t *__restrict__ offsets, W4Shape p,
     void *__restrict__ y) {
     constexpr int kCols = 16 / kSegs;  // rows of x and output columns of a tile
+    // A tile's scales: kPer words of each of the 16 code rows (four E8M0 bytes
+    // or one FP32 number per block), kScaleLoads of them a lane.
+    constexpr int kScaleLoads = (16 * kPer + 63) / 64;
     __shared__ float sums[2][kWaves][16][17];
-    __shared__ __attribute__((aligned(16))) uint16_t end_of_x[kCols][kBlockK];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    __shared__ __attribute__((aligned(16))) uint16_t end_of_x[16][kBlockK];
+    __shared__ u32x4 lds_codes[kWaves][kPer < 4 ? 4 * 64 : kPer * 64];
+    __shared__ uint32_t lds_scales[kWaves][kScaleLoads * 64];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int c = lane & 15, q = lane >> 4;
-    const int col = c % kCols, seg = c / kCols;
     const int split = 1 << p.split_log, tiles_each = kWaves >> p.split_log;
     const int along = wave & (split - 1), sub = wave >> p.split_log;
     int e = 0, r0 = 0, r1 = p.R;
     if (offsets) busy_expert(offsets, p.E, p.R, blockIdx.y, e, r0, r1);
 
-    const int64_t row_bytes = (p.K + 1) / 2, all_rows = p.E * p.N;
-    const int groups = kE8m0 ? (int)((p.K + 31) / 32) : p.blocks;
+    const int64_t row_bytes = (p.K + 1) / 2;
+    const int64_t scale_bytes = kE8m0 ? (p.K + 31) / 32 : 4 * (int64_t)p.blocks;
+    const uint8_t *codes_end = codes + p.E * p.N * row_bytes;
+    const uint8_t *scales_end = scales + p.E * p.N * scale_bytes;
     const int stretches = split * kSegs;
     const int64_t tile0 = (int64_t)blockIdx.x * p.steps * tiles_each + sub;
     const int full = (int)(p.K / kBlockK);  // whole blocks; one more, in part, if blocks > full
+    u32x4 *my_codes = lds_codes[wave];
+    uint32_t *my_scales = lds_scales[wave];
+
+    // Operand row r is output column r % kCols in stretch r / kCols.
+    auto first_block = [&](int r, int chunk) {
+        return (chunk * stretches + along * kSegs + r / kCols) * kPer;
+    };
+    // A tile begins at column tile * kCols, or as many columns before the last
+    // one as it has (columns it shares with the tile before it are not stored
+    // again); a matrix of fewer columns reads its last one again.
+    auto first_column = [&](int64_t tile) {
+        const int64_t n = tile * kCols, most = p.N > kCols ? p.N - kCols : 0;
+        return n < most ? n : most;
+    };
+
+    // Byte offsets of this lane's 16 bytes of each load within a tile (K below
+    // 2^24 keeps them in 32 bits), and of its scale words.
+    uint32_t code_at[kPer], scale_at[kScaleLoads];
+    auto place = [&](int chunk) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int j = 64 * i + lane, r = j / (4 * kPer);
+            const int n = min(r % kCols, (int)(p.N < 16 ? p.N : 16) - 1);
+            code_at[i] = n * (uint32_t)row_bytes + first_block(r, chunk) * 64u + j % (4 * kPer) * 16u;
+        }
+#pragma unroll
+        for (int i = 0; i < kScaleLoads; ++i) {
+            const int j = min(64 * i + lane, 16 * kPer - 1), r = j / kPer;
+            const int n = min(r % kCols, (int)(p.N < 16 ? p.N : 16) - 1);
+            scale_at[i] = n * (uint32_t)scale_bytes + (first_block(r, chunk) + j % kPer) * 4u;
+        }
+    };
+    u32x4 code[kPer];
+    uint32_t scale[kScaleLoads];
+    // What lies past the end of a row (and in blocks past its last one) meets
+    // zeros of x, so only a read past the end of the whole array is avoided:
+    // it begins earlier and is moved down before it is used.
+    auto near_end = [&](int64_t tile) {
+        return (e * p.N + first_column(tile) + kCols) * row_bytes + 64ll * kPer * stretches * p.chunks
+                   > p.E * p.N * row_bytes;
+    };
+    auto load_tile = [&](int64_t tile) {
+        const int64_t row = e * p.N + first_column(tile);
+        const uint8_t *from = codes + row * row_bytes, *scale_from = scales + row * scale_bytes;
+        if (near_end(tile)) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const uint8_t *at = from + code_at[i];
+                code[i] = *reinterpret_cast<const u32x4_any *>(at - end_back<16>(codes_end - at));
+            }
+#pragma unroll
+            for (int i = 0; i < kScaleLoads; ++i) {
+                const uint8_t *at = scale_from + scale_at[i];
+                scale[i] =
+                    *reinterpret_cast<const u32_any *>(at - end_back<4>(scales_end - at));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                code[i] = *reinterpret_cast<const u32x4_any *>(from + code_at[i]);
+#pragma unroll
+            for (int i = 0; i < kScaleLoads; ++i)
+                scale[i] = *reinterpret_cast<const u32_any *>(scale_from + scale_at[i]);
+        }
+    };
+    // Loaded registers to the wave's LDS.
+    auto keep_tile = [&](int64_t tile) {
+        if (near_end(tile)) {
+            const int64_t row = e * p.N + first_column(tile);
+            const uint8_t *from = codes + row * row_bytes, *scale_from = scales + row * scale_bytes;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                code[i] = shift_down(
+                    code[i], min(end_back<16>(codes_end - (from + code_at[i])), 16));
+#pragma unroll
+            for (int i = 0; i < kScaleLoads; ++i) {
+                const int back = end_back<4>(scales_end - (scale_from + scale_at[i]));
+                scale[i] = back < 4 ? scale[i] >> (8 * back) : 0;
+            }
+        }
+        wave_order();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) my_codes[64 * i + lane] = code[i];
+#pragma unroll
+        for (int i = 0; i < kScaleLoads; ++i) my_scales[64 * i + lane] = scale[i];
+        wave_order();
+    };
 
     for (int m0 = r0; m0 < r1; m0 += kCols) {
         const int rows = min(kCols, r1 - m0);
-        const Bf16 *xrow = x + (int64_t)(m0 + min(col, rows - 1)) * p.ldx;
         bf16x8 held[kPer][4];
-        u32x4 code[kPer];
-        uint32_t scale[kPer];  // as loaded: E8M0 byte or FP32 bits
 
-        // the first block of this lane's stretch in pass `chunk`
-        auto first_block = [&](int chunk) {
-            return (chunk * stretches + along * kSegs + seg) * kPer;
-        };
         // x is zero past K: the block that K ends in is brought to LDS with
         // its zeros, once for these rows.
         if (p.blocks > full) {
-            for (int i = threadIdx.x; i < kCols * kBlockK; i += 64 * kWaves) {
+            for (int i = threadIdx.x; i < 16 * kBlockK; i += 64 * kWaves) {
                 const int m = i / kBlockK, k = i % kBlockK;
                 const int64_t at = (int64_t)full * kBlockK + k;
                 end_of_x[m][k] =
@@ -220,81 +326,60 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
             }
             __syncthreads();
         }
-        // Lanes of rows past the last stay zero and idle: with one row the
-        // loads touch a sixteenth of the lanes.
+        // Also read along the rows, 16 lanes to the 256 bytes of a block, and
+        // turned in the wave's LDS; rows past the last are zero and not read.
         auto load_x = [&](int chunk) {
-            const int b0 = first_block(chunk);
-            const Bf16 *from = xrow + (int64_t)b0 * kBlockK + 32 * q;
+            constexpr int kAtOnce = kPer < 4 ? kPer : 4;
 #pragma unroll
-            for (int b = 0; b < kPer; ++b) {
-                u32x4 v[4] = {};
-                if (b0 + b < full && col < rows) {
+            for (int b0 = 0; b0 < kPer; b0 += kAtOnce) {
+                u32x4 v[kAtOnce][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[i] = *reinterpret_cast<const u32x4_any *>(from + b * kBlockK + 8 * i);
+                for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (b0 + j >= kPer) continue;
+                        const int r = 4 * i + q, m = r % kCols;
+                        const int block = first_block(r, chunk) + b0 + j;
+                        v[j][i] = u32x4{0, 0, 0, 0};
+                        if (m < rows && block < full)
+                            v[j][i] = *reinterpret_cast<const u32x4_any *>(
+                                x + (int64_t)(m0 + m) * p.ldx + (int64_t)block * kBlockK + 8 * c);
+                    }
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j) {
+                    if (b0 + j >= kPer) continue;
+                    // unit u (16 bytes) of row r at u ^ r: all rows begin on the same banks
+                    wave_order();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 4 * i + q;
+                        my_codes[16 * r + (c ^ r)] = v[j][i];
+                    }
+                    wave_order();
+                    const bool last = p.blocks > full && first_block(c, chunk) + b0 + j == full;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        u32x4 t = my_codes[16 * c + ((4 * q + i) ^ c)];
+                        if (last)
+                            t = *reinterpret_cast<const u32x4 *>(
+                                &end_of_x[c % kCols][32 * q + 8 * i]);
+                        held[b0 + j][i] = __builtin_bit_cast(bf16x8, t);
+                    }
                 }
-                if (p.blocks > full && b0 + b == full) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[i] = *reinterpret_cast<const u32x4 *>(&end_of_x[col][32 * q + 8 * i]);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) held[b][i] = __builtin_bit_cast(bf16x8, v[i]);
             }
-        };
-        // Where this lane's blocks of a tile begin.  Blocks past the row's last
-        // one read that again (x is zero there); what lies past the end of a
-        // row meets zeros of x as well.  Only the last block of the last rows
-        // could reach past the end of all codes: there the 16 bytes begin
-        // `back` bytes earlier, to be moved down before they are used.
-        const uint8_t *from;
-        const void *scale_from;
-        int end, back, last, last_group;
-        auto place = [&](int64_t tile, int chunk) {
-            const int b0 = first_block(chunk);
-            int64_t n = tile * kCols + col;
-            n = n < p.N ? n : p.N - 1;  // a column past the end is not stored
-            const int64_t row = e * p.N + n;
-            const int64_t at = (int64_t)b0 * 64 + 16 * q;
-            from = codes + row * row_bytes + at;
-            last = p.blocks - 1 - b0;
-            const int64_t left = (all_rows - row) * row_bytes - at - 64 * (int64_t)last;
-            back = left < 16 ? 16 - (int)left : 0;
-            end = 64 * last - back;
-            if (kE8m0) {
-                const int g = 4 * b0 + q;
-                scale_from = static_cast<const uint8_t *>(scales) + row * groups + g;
-                last_group = groups - 1 - g;
-            } else {
-                scale_from = static_cast<const float *>(scales) + row * groups + b0;
-            }
-        };
-        auto load_weights = [&](int b) {
-            code[b] = *reinterpret_cast<const u32x4_any *>(from + min(64 * b, end));
-            if (kE8m0)
-                scale[b] = static_cast<const uint8_t *>(scale_from)[min(4 * b, last_group)];
-            else
-                scale[b] = static_cast<const uint32_t *>(scale_from)[min(b, last)];
         };
 
         f32x4 acc = {0, 0, 0, 0};
         int buffer = 0;
-        // One tile (of one pass): unpack, ask for the next one's codes, add up.
-        auto products = [&](int cut, int cut_back, auto more) {
-            if (__any(cut >= 0 && cut < kPer)) {
-#pragma unroll
-                for (int b = 0; b < kPer; ++b)
-                    if (b == cut) code[b] = shift_down(code[b], cut_back);
-            }
+        auto products = [&] {
 #pragma unroll
             for (int b = 0; b < kPer; ++b) {
-                const float s = __uint_as_float(kE8m0 ? scale[b] << 23 : scale[b]);
+                const u32x4 code = my_codes[4 * kPer * c + 4 * b + q];
+                const uint32_t word = my_scales[kPer * c + b];
+                const float s = __uint_as_float(kE8m0 ? (word >> (8 * q) & 0xFF) << 23 : word);
                 bf16x8 w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = weights8(code[b][i], kE8m0 ? s : 1.0f);
-                __builtin_amdgcn_sched_barrier(0);
-                if constexpr (decltype(more)::value) load_weights(b);
-                __builtin_amdgcn_sched_barrier(0);
+                for (int i = 0; i < 4; ++i) w[i] = weights8(code[i], kE8m0 ? s : 1.0f);
                 if (kE8m0) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -321,8 +406,8 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
             for (int o = threadIdx.x; o < tiles_each * rows * kCols; o += 64 * kWaves) {
                 const int which = o / (rows * kCols);
                 const int m = o / kCols % rows, n = o % kCols;
-                const int64_t at = (first + which) * kCols + n;
-                if (at >= p.N) continue;
+                const int64_t at = first_column(first + which) + n;
+                if (at >= p.N || at < (first + which) * kCols) continue;
                 float sum = 0;
                 for (int w = 0; w < split; ++w)
 #pragma unroll
@@ -336,31 +421,34 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
             acc = f32x4{0, 0, 0, 0};
         };
 
-        place(tile0, 0);
-#pragma unroll
-        for (int b = 0; b < kPer; ++b) load_weights(b);
+        place(0);
+        load_tile(tile0);
         load_x(0);
         const int64_t units = (int64_t)p.steps * p.chunks;
         int chunk = 0;
         int64_t tile = tile0;
-        for (int64_t u = 1; u < units; ++u) {
-            const int cut = back > 0 ? last : -1, cut_back = min(back, 16);
+        for (int64_t u = 0; u < units; ++u) {
+            keep_tile(tile);
             const int64_t done = tile;
-            if (kChunked) chunk = chunk + 1 < p.chunks ? chunk + 1 : 0;
-            if (!kChunked || chunk == 0) tile += tiles_each;
-            place(tile, chunk);
-            products(cut, cut_back, std::true_type{});
-            if (kChunked) load_x(chunk);
-            if (!kChunked || chunk == 0) store(done);
+            if (u + 1 < units) {
+                if (kChunked) {
+                    chunk = chunk + 1 < p.chunks ? chunk + 1 : 0;
+                    place(chunk);
+                }
+                if (!kChunked || chunk == 0) tile += tiles_each;
+                load_tile(tile);
+            }
+            products();
+            if (kChunked && u + 1 < units) load_x(chunk);
+            if (!kChunked || chunk == 0 || u + 1 == units) store(done);
         }
-        products(back > 0 ? last : -1, min(back, 16), std::false_type{});
-        store(tile);
         __syncthreads();  // the next rows begin with the first buffer again
     }
 }
 
-// Codes of fewer than 16 bytes in all (or none): the kernel above reads 16 at
-// a time.  One thread a sum of at most 30 products.
+// Codes of fewer than 16 bytes in all, or E8M0 scales of fewer than 4: the
+// kernel above reads as many at a time.  One thread a sum of at most 96
+// products (or of none).
 template <bool kE8m0>
 __global__ __launch_bounds__(256) void w4_few_codes_kernel(
     const Bf16 *__restrict__ x, const uint8_t *__restrict__ codes,
@@ -385,7 +473,7 @@ __global__ __launch_bounds__(256) void w4_few_codes_kernel(
             const float s = kE8m0 ? __uint_as_float((uint32_t)static_cast<const uint8_t *>(
                                                         scales)[row * ((p.K + 31) / 32) + k / 32]
                                                     << 23)
-                                  : static_cast<const float *>(scales)[row];
+                                  : static_cast<const float *>(scales)[row * ((p.K + 127) / 128) + k / 128];
             const bf16x2 w =
                 __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code & 15, kE8m0 ? s : 1.0f, 0);
             const float value = kE8m0 ? (float)w[0] : s * (float)w[0];
@@ -398,7 +486,7 @@ __global__ __launch_bounds__(256) void w4_few_codes_kernel(
 
 // The kernel for `segs` stretches side by side of `per` blocks each (rounded
 // up to one that is built; the blocks too many are read twice, times zero).
-using MatvecKernel = void (*)(const Bf16 *, const uint8_t *, const void *, const int32_t *,
+using MatvecKernel = void (*)(const Bf16 *, const uint8_t *, const uint8_t *, const int32_t *,
                               W4Shape, void *);
 template <bool kE8m0>
 MatvecKernel matvec_kernel(int segs, int &per, bool chunked) {
@@ -445,7 +533,8 @@ hipError_t launch_w4_matvec(const void *x, int64_t ldx, const void *codes, const
     p.bf16_out = bf16_out;
     const Bf16 *rows = static_cast<const Bf16 *>(x);
     const uint8_t *bytes = static_cast<const uint8_t *>(codes);
-    if (K == 0 || E * N * ((K + 1) / 2) < 16) {
+    const uint8_t *scale_bytes = static_cast<const uint8_t *>(scales);
+    if (K == 0 || E * N * ((K + 1) / 2) < 16 || E * N * ((K + 31) / 32) < 4) {
         const int64_t sums = R * N < (1 << 22) ? R * N : (1 << 22);
         auto *kernel = e8m0 ? w4_few_codes_kernel<true> : w4_few_codes_kernel<false>;
         kernel<<<(unsigned)((sums + 255) / 256), 256, 0, stream>>>(rows, bytes, scales, offsets, p,
@@ -477,10 +566,10 @@ hipError_t launch_w4_matvec(const void *x, int64_t ldx, const void *codes, const
     p.chunks = (p.blocks + stretches * per - 1) / (stretches * per);
     const int64_t total = groups() / active;  // workgroups of an expert at one step each
     p.steps = 1;
-    const int64_t target = offsets ? 1024 : 512;
+    const int64_t target = offsets ? 1024 : 256;
     if (total * active > target) p.steps = (int)((total * active + target - 1) / target);
     const dim3 grid((unsigned)((total + p.steps - 1) / p.steps), (unsigned)active);
-    kernel<<<grid, 64 * kWaves, 0, stream>>>(rows, bytes, scales, offsets, p, y);
+    kernel<<<grid, 64 * kWaves, 0, stream>>>(rows, bytes, scale_bytes, offsets, p, y);
     return hipGetLastError();
 }
 
