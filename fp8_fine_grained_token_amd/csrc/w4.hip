@@ -271,7 +271,8 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 const uint8_t *at = from + code_at[i];
-                code[i] = *reinterpret_cast<const u32x4_any *>(at - end_back<16>(codes_end - at));
+                code[i] = __builtin_nontemporal_load(
+                    reinterpret_cast<const u32x4_any *>(at - end_back<16>(codes_end - at)));
             }
 #pragma unroll
             for (int i = 0; i < kScaleLoads; ++i) {
@@ -282,7 +283,8 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
         } else {
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-                code[i] = *reinterpret_cast<const u32x4_any *>(from + code_at[i]);
+                code[i] = __builtin_nontemporal_load(
+                    reinterpret_cast<const u32x4_any *>(from + code_at[i]));
 #pragma unroll
             for (int i = 0; i < kScaleLoads; ++i)
                 scale[i] = *reinterpret_cast<const u32_any *>(scale_from + scale_at[i]);
@@ -330,6 +332,14 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
         // turned in the wave's LDS; rows past the last are zero and not read.
         auto load_x = [&](int chunk) {
             constexpr int kAtOnce = kPer < 4 ? kPer : 4;
+            const Bf16 *from[4];
+            int whole[4];  // blocks to read of row 4 i + q
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 4 * i + q, m = r % kCols, first = first_block(r, chunk);
+                from[i] = x + (int64_t)(m0 + m) * p.ldx + (int64_t)first * kBlockK + 8 * c;
+                whole[i] = m < rows ? full - first : 0;
+            }
 #pragma unroll
             for (int b0 = 0; b0 < kPer; b0 += kAtOnce) {
                 u32x4 v[kAtOnce][4];
@@ -338,12 +348,10 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if (b0 + j >= kPer) continue;
-                        const int r = 4 * i + q, m = r % kCols;
-                        const int block = first_block(r, chunk) + b0 + j;
                         v[j][i] = u32x4{0, 0, 0, 0};
-                        if (m < rows && block < full)
-                            v[j][i] = *reinterpret_cast<const u32x4_any *>(
-                                x + (int64_t)(m0 + m) * p.ldx + (int64_t)block * kBlockK + 8 * c);
+                        if (b0 + j < whole[i])
+                            v[j][i] = *reinterpret_cast<const u32x4_any *>(from[i] +
+                                                                           (b0 + j) * kBlockK);
                     }
 #pragma unroll
                 for (int j = 0; j < kAtOnce; ++j) {
@@ -421,12 +429,15 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
             acc = f32x4{0, 0, 0, 0};
         };
 
-        place(0);
-        load_tile(tile0);
-        load_x(0);
         const int64_t units = (int64_t)p.steps * p.chunks;
         int chunk = 0;
         int64_t tile = tile0;
+        // (keeps these loads here: taken out of the loop over rows, where there
+        // is but one pass as a rule, they were spilled one by one)
+        asm volatile("" : "+s"(tile));
+        place(0);
+        load_tile(tile);
+        load_x(0);
         for (int64_t u = 0; u < units; ++u) {
             keep_tile(tile);
             const int64_t done = tile;
