@@ -101,11 +101,9 @@ fp8_status sort_dispatch_quant(const void *x, int64_t ldx, int64_t T, int64_t H,
         if (!aligned(scales, 4)) return FP8_ERR_ALIGN;
     }
     clear_last_error();
-    hipError_t e = launch_moe_sort(r, as_stream(stream));
-    if (e == hipSuccess && rows)
-        e = launch_moe_dispatch_quant(x, ldx, T, H, slot_row, k, q, scales, T * k, pow2,
-                                      as_stream(stream));
-    return from_hip(e);
+    if (!rows) return from_hip(launch_moe_sort(r, as_stream(stream)));
+    return from_hip(
+        launch_moe_sort_dispatch_quant(r, x, ldx, H, q, scales, pow2, as_stream(stream)));
 }
 
 // ---- norms ----
@@ -266,11 +264,10 @@ fp8_status fp8_moe_sort_dispatch(const void *x, int elem_bytes, int64_t ldx, int
         if (!aligned(xs, elem_bytes)) return FP8_ERR_ALIGN;
     }
     clear_last_error();
-    hipError_t e = launch_moe_sort(r, as_stream(hip_stream));
-    if (e == hipSuccess && rows)
-        e = launch_moe_dispatch(GatherPlane{x, xs, H * elem_bytes, ldx * elem_bytes, elem_bytes},
-                                nullptr, slot_row, T, top_k, T * top_k, as_stream(hip_stream));
-    return from_hip(e);
+    if (!rows) return from_hip(launch_moe_sort(r, as_stream(hip_stream)));
+    return from_hip(launch_moe_sort_dispatch(
+        r, GatherPlane{x, xs, H * elem_bytes, ldx * elem_bytes, elem_bytes},
+        as_stream(hip_stream)));
 }
 
 fp8_status fp8_moe_sort_dispatch_quant_1x128(const void *x_bf16, int64_t ldx, int64_t T,

@@ -36,6 +36,13 @@ hipError_t launch_moe_dispatch_quant(const void *x, int64_t ldx, int64_t T, int6
                                      const int32_t *slot_row, int64_t k, void *q, float *scales,
                                      int64_t R, bool pow2, hipStream_t stream);
 
+// Sort and gather: one launch for few slots.
+hipError_t launch_moe_sort_dispatch(const MoeRouting &r, const GatherPlane &rows,
+                                    hipStream_t stream);
+hipError_t launch_moe_sort_dispatch_quant(const MoeRouting &r, const void *x, int64_t ldx,
+                                          int64_t H, void *q, float *scales, bool pow2,
+                                          hipStream_t stream);
+
 hipError_t launch_moe_combine(const void *ys, bool ys_bf16, int64_t ld, int64_t R,
                               const int32_t *slot_row, const float *weights, int64_t T,
                               int64_t k, int64_t H, const void *residual, int64_t ld_residual,

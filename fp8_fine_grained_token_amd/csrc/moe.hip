@@ -198,13 +198,17 @@ hipError_t sort_typed(const MoeRouting &r, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// ---- gather ----------------------------------------------------------------
-
+// ---- rows and their parts ---------------------------------------------------
+//
+// A row is taken in vectors of 16 bytes (the copies) or eight values (the
+// rest), one a thread: tx threads (a power of two) to a row and 256 / tx rows
+// to a workgroup, the workgroups of gridDim.y side by side along wide rows.
+// A token's slots are read kBatch at a time, the row numbers of a batch in
+// one go and then the rows, so that a wait covers a batch and not a slot.
 constexpr int kRowThreads = 256;
+constexpr int kBatch = 8;
 constexpr int64_t kMaxBlocks = (int64_t)1 << 22;
 
-// A workgroup of 256 threads takes 256 / tx tokens, tx (a power of two)
-// threads to a row; the rows past the grid by strides.
 struct RowShape {
     int64_t T;
     int tx_log;
@@ -216,160 +220,375 @@ inline int log2_of(int v) {
     return l;
 }
 
-inline unsigned row_blocks(int64_t T, int tx) {
-    const int64_t per = kRowThreads / tx;
-    const int64_t blocks = (T + per - 1) / per;
-    return (unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks);
+// Threads and workgroups for T rows of `vecs` vectors.
+struct RowGrid {
+    RowShape shape;
+    dim3 grid;
+};
+
+RowGrid row_grid(int64_t T, int64_t vecs, int least) {
+    const int tx = threads_per_row(vecs, least, kRowThreads);
+    const int64_t per = kRowThreads / tx, blocks = (T + per - 1) / per;
+    const int64_t along = (vecs + tx - 1) / tx;
+    RowGrid g;
+    g.shape = {T, log2_of(tx)};
+    g.grid = dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks),
+                  (unsigned)(along < 65535 ? along : 65535));
+    return g;
 }
 
-__device__ __forceinline__ void copy_row(const GatherPlane &g, int64_t t, int64_t T, int64_t k,
-                                         const int32_t *slot_row, int64_t R, int lane, int tx) {
-    const uint8_t *src = static_cast<const uint8_t *>(g.src) + t * g.ld;
-    uint8_t *dst = static_cast<uint8_t *>(g.dst);
-    const int64_t vecs = (g.bytes + 15) / 16;
-    for (int64_t v = lane; v < vecs; v += tx) {
-        const int64_t at = 16 * v;
-        if (at + 16 <= g.bytes) {
-            const u32x4_any d = *reinterpret_cast<const u32x4_any *>(src + at);
-            for (int64_t j = 0; j < k; ++j) {
-                const int32_t row = slot_row[t * k + j];
-                if (row >= 0 && row < R)
-                    *reinterpret_cast<u32x4_any *>(dst + row * g.bytes + at) = d;
-            }
-        } else {
-            for (int64_t j = 0; j < k; ++j) {
-                const int32_t row = slot_row[t * k + j];
-                if (row >= 0 && row < R)
-                    for (int64_t i = at; i < g.bytes; ++i) dst[row * g.bytes + i] = src[i];
+// The rows of slots j0 .. of token t, -1 for a dropped slot (or none), and
+// their weights.  A token has at least 16 lanes of a wave: lane b of each 16
+// reads slot b and hands it round, so one load brings a batch.
+template <int kCount>
+struct Batch {
+    static_assert(kCount <= 16, "a batch is read by 16 lanes");
+    int32_t rows[kCount];
+    float w[kCount];
+    int32_t my_row;
+    float my_w;
+    __device__ __forceinline__ void load(const int32_t *slot_row, const float *weights, int64_t t,
+                                         int64_t k, int64_t j0) {
+        const int64_t lane = threadIdx.x & 15, j = j0 + lane < k ? j0 + lane : k - 1;
+        my_w = 1.0f;
+        if (weights) my_w = weights[t * k + j];
+        my_row = slot_row[t * k + j];
+    }
+    __device__ __forceinline__ void share(int64_t k, int64_t j0, int64_t R) {
+        const int64_t lane = threadIdx.x & 15;
+        const int32_t row = j0 + lane < k && my_row >= 0 && my_row < R ? my_row : -1;
+#pragma unroll
+        for (int b = 0; b < kCount; ++b) {
+            rows[b] = __shfl(row, b, 16);
+            w[b] = __shfl(my_w, b, 16);
+        }
+    }
+};
+
+// ---- gather ----------------------------------------------------------------
+
+enum GatherMode { kCopy, kQuant, kQuantPow2 };
+
+// Quantizing rows of fewer than eight values or more (a copy does not ask).
+template <int kMode, bool kNarrow>
+struct Gather {
+    static constexpr bool copy = kMode == kCopy, pow2 = kMode == kQuantPow2, narrow = kNarrow;
+};
+
+struct GatherArgs {
+    GatherPlane rows, scales;  // copy
+    const Bf16 *x;             // quantize
+    int64_t ldx, H;
+    uint8_t *q;
+    float *q_scales;
+    int64_t k, R;
+};
+
+__device__ __forceinline__ int64_t plane_vecs(const GatherPlane &g) { return (g.bytes + 15) / 16; }
+
+// Bytes 16 v .. of token t's row to the rows of its slots (the row's last 16
+// bytes for its last vector); get(j0, rows) gives a batch of them.
+template <typename Rows>
+__device__ __forceinline__ void copy_vec(const GatherPlane &g, int64_t t, int64_t v, bool in,
+                                         int64_t k, Rows get) {
+    const bool wide = g.bytes >= 16;
+    in = in && 16 * v < g.bytes;
+    const int64_t at = wide ? (16 * v < g.bytes - 16 ? 16 * v : g.bytes - 16) : 0;
+    const uint8_t *src = static_cast<const uint8_t *>(g.src) + t * g.ld + at;
+    uint8_t *dst = static_cast<uint8_t *>(g.dst) + at;
+    u32x4_any d = {0, 0, 0, 0};
+    if (wide) d = *reinterpret_cast<const u32x4_any *>(src);
+    for (int64_t j0 = 0; j0 < k; j0 += kBatch) {
+        int32_t rows[kBatch];
+        get(j0, rows);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (rows[b] < 0 || !in) continue;
+            if (wide) {
+                *reinterpret_cast<u32x4_any *>(dst + rows[b] * g.bytes) = d;
+            } else {
+                for (int i = 0; i < (int)g.bytes; ++i) dst[rows[b] * g.bytes + i] = src[i];
             }
         }
     }
 }
 
-__global__ __launch_bounds__(kRowThreads) void dispatch_kernel(GatherPlane rows,
-                                                               GatherPlane scales, RowShape shape,
-                                                               const int32_t *__restrict__ slot_row,
-                                                               int64_t k, int64_t R) {
-    const int tx = 1 << shape.tx_log, lane = threadIdx.x & (tx - 1);
-    const int64_t per = kRowThreads >> shape.tx_log;
-    for (int64_t t = blockIdx.x * per + (threadIdx.x >> shape.tx_log); t < shape.T;
-         t += gridDim.x * per) {
-        copy_row(rows, t, shape.T, k, slot_row, R, lane, tx);
-        if (scales.src) copy_row(scales, t, shape.T, k, slot_row, R, lane, tx);
+// Vector v of token t quantized (16 lanes hold one 128-value group, eight
+// values each, as in the activation quantizer), for all lanes of a wave or
+// none: the 16-lane maximum needs its lanes.
+template <bool kPow2, bool kNarrow, typename Rows>
+__device__ __forceinline__ void quant_vec(const GatherArgs &a, int64_t t, int64_t v, bool in,
+                                          Rows get) {
+    const int64_t G = (a.H + kGroup - 1) / kGroup;
+    const Span s = row_span(v, a.H);
+    Raw8<Bf16> raw;
+    load_raw<kNarrow>(a.x + t * a.ldx + s.col, s.hi, raw);
+    float f[8];
+    unpack_own(raw, s, f);
+    const QuotientCtx qc(row16_max(absmax8(f)), kPow2);
+    const uint2 bytes = quant8(f, qc);
+    in = in && s.any();
+    for (int64_t j0 = 0; j0 < a.k; j0 += kBatch) {
+        int32_t rows[kBatch];
+        get(j0, rows);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (rows[b] < 0 || !in) continue;
+            store_e4m3(a.q + rows[b] * a.H, s, bytes);
+            if ((threadIdx.x & 15) == 0) a.q_scales[rows[b] * G + v / 16] = qc.s;
+        }
     }
 }
 
-// Quantized: 16 lanes hold one 128-value group, eight values each, as in the
-// activation quantizer; every lane of a wave takes the same number of turns,
-// so the 16-lane maximum always has its lanes.
-template <bool kPow2>
-__global__ __launch_bounds__(kRowThreads) void dispatch_quant_kernel(
-    const Bf16 *__restrict__ x, int64_t ldx, RowShape shape, int64_t H,
-    const int32_t *__restrict__ slot_row, int64_t k, uint8_t *__restrict__ q,
-    float *__restrict__ scales, int64_t R) {
+template <typename M>
+__global__ __launch_bounds__(kRowThreads) void dispatch_kernel(GatherArgs a, RowShape shape,
+                                                               const int32_t *__restrict__ slot_row) {
     const int tx = 1 << shape.tx_log, lane = threadIdx.x & (tx - 1);
-    const int64_t per = kRowThreads >> shape.tx_log;
-    const int64_t G = (H + kGroup - 1) / kGroup, vecs = 16 * G;
-    const int64_t rounds = (shape.T + per - 1) / per;
+    const int64_t per = kRowThreads >> shape.tx_log, rounds = (shape.T + per - 1) / per;
     for (int64_t b = blockIdx.x; b < rounds; b += gridDim.x) {
-        const int64_t t = b * per + (threadIdx.x >> shape.tx_log);
-        const bool in = t < shape.T;
-        for (int64_t v0 = 0; v0 < vecs; v0 += tx) {
-            const int64_t v = v0 + lane;
-            const int n = in ? vec_count(H, v) : 0;
-            float f[8];
-            load8(x + t * ldx + 8 * v, n, f);
-            const QuotientCtx qc(row16_max(absmax8(f)), kPow2);
-            const uint2 bytes = quant8(f, qc);
-            if (!in || v >= vecs) continue;
-            for (int64_t j = 0; j < k; ++j) {
-                const int32_t row = slot_row[t * k + j];
-                if (row < 0 || row >= R) continue;
-                store_e4m3(q + row * H + 8 * v, n, bytes);
-                if ((lane & 15) == 0) scales[row * G + v / 16] = qc.s;
-            }
+        const int64_t own = b * per + (threadIdx.x >> shape.tx_log);
+        const bool in = own < shape.T;
+        const int64_t t = in ? own : shape.T - 1;
+        auto get = [&](int64_t j0, int32_t(&rows)[kBatch]) {
+            Batch<kBatch> batch;
+            batch.load(slot_row, nullptr, t, a.k, j0);
+            batch.share(a.k, j0, a.R);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) rows[i] = batch.rows[i];
+        };
+        const int64_t v0 = (int64_t)blockIdx.y * tx, step = (int64_t)gridDim.y * tx;
+        // every lane stays to the end: lanes hand each other row numbers
+        if (M::copy) {
+            for (int64_t v = v0; v < plane_vecs(a.rows); v += step)
+                copy_vec(a.rows, t, v + lane, in, a.k, get);
+            if (a.scales.src)
+                for (int64_t v = v0; v < plane_vecs(a.scales); v += step)
+                    copy_vec(a.scales, t, v + lane, in, a.k, get);
+        } else {
+            for (int64_t v = v0; v < 16 * ((a.H + kGroup - 1) / kGroup); v += step)
+                quant_vec<M::pow2, M::narrow>(a, t, v + lane, in, get);
         }
     }
+}
+
+// Sort and gather of few slots in one launch.  The row of slot (t, j) is the
+// number of kept slots that come before it in the order (expert, slot): every
+// workgroup of a token counts them for the token's own slots by going through
+// all ids (kFewSlots of them are 32 KiB from L2), so there is no launch
+// between the sort and the gather and nothing to wait for.  One more row of
+// workgroups writes the offsets.
+constexpr int64_t kFewSlots = 4096;
+
+template <typename M, typename Id>
+__global__ __launch_bounds__(kRowThreads) void sort_dispatch_kernel(
+    GatherArgs a, const Id *__restrict__ ids, int T, int E, int32_t *__restrict__ offsets,
+    int32_t *__restrict__ slot_row, int32_t *__restrict__ row_slot) {
+    constexpr int kWaves = kRowThreads / 64;
+    __shared__ int32_t hist[kSortMaxExperts];
+    __shared__ int32_t part[kWaves][kBatch];
+    const int k = (int)a.k, slots = T * k;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if ((int)blockIdx.x == T) {
+        if (blockIdx.y) return;
+        for (int e = threadIdx.x; e < E; e += kRowThreads) hist[e] = 0;
+        __syncthreads();
+        for (int s = threadIdx.x; s < slots; s += kRowThreads) {
+            const int e = expert_of(ids, s, E);
+            if (e >= 0) atomicAdd(&hist[e], 1);
+        }
+        __syncthreads();
+        constexpr int kPer = kSortMaxExperts / kRowThreads;
+        int32_t sum = 0;
+        for (int i = 0; i < kPer; ++i) {
+            const int e = (int)threadIdx.x * kPer + i;
+            sum += e < E ? hist[e] : 0;
+        }
+        int32_t up = sum;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int32_t v = __shfl_up(up, d);
+            if (lane >= d) up += v;
+        }
+        if (lane == 63) part[wave][0] = up;
+        __syncthreads();
+        int32_t start = up - sum, total = 0;
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < wave) start += part[w][0];
+            total += part[w][0];
+        }
+        for (int i = 0; i < kPer; ++i) {
+            const int e = (int)threadIdx.x * kPer + i;
+            if (e < E) {
+                offsets[e] = start;
+                start += hist[e];
+            }
+        }
+        if (threadIdx.x == 0) offsets[E] = total;
+        for (int r = total + threadIdx.x; r < slots; r += kRowThreads) row_slot[r] = -1;
+        return;
+    }
+    const int t = blockIdx.x;
+    auto get = [&](int64_t j0, int32_t(&rows)[kBatch]) {
+        // key (expert, slot): below 1024 * 4096
+        int key[kBatch], count[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int s = t * k + min((int)j0 + b, k - 1);
+            const int e = (int)j0 + b < k ? expert_of(ids, s, E) : -1;
+            key[b] = e < 0 ? -1 : e * slots + s;
+            count[b] = 0;
+        }
+        for (int s0 = wave * 64; s0 < slots; s0 += kRowThreads) {
+            const int s = s0 + lane;
+            const int e = s < slots ? expert_of(ids, s, E) : -1;
+            const int other = e < 0 ? 0x7FFFFFFF : e * slots + s;
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) count[b] += __popcll(__ballot(other < key[b]));
+        }
+        __syncthreads();  // the last batch's reads
+        if (lane == 0)
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) part[wave][b] = count[b];
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            int row = 0;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) row += part[w][b];
+            rows[b] = key[b] < 0 ? -1 : row;
+        }
+        if (blockIdx.y == 0 && (int)threadIdx.x < kBatch && (int)j0 + (int)threadIdx.x < k) {
+            int row = -1;
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+                if ((int)threadIdx.x == b) row = rows[b];
+            const int s = t * k + (int)j0 + (int)threadIdx.x;
+            slot_row[s] = row;
+            if (row >= 0) row_slot[row] = s;
+        }
+    };
+    // one vector a thread: the grid covers the row
+    const int64_t v = (int64_t)blockIdx.y * kRowThreads + threadIdx.x;
+    if (M::copy)
+        copy_vec(a.rows, t, v, true, a.k, get);  // past the row's end: counts, copies nothing
+    else
+        quant_vec<M::pow2, M::narrow>(a, t, v, true, get);
 }
 
 // ---- weighted sum back, and the gradients -------------------------------------
 
-template <typename In, typename Out>
+template <typename In, typename Out, bool kNarrow>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(
     const In *__restrict__ ys, int64_t ld, int64_t R, const int32_t *__restrict__ slot_row,
     const float *__restrict__ weights, RowShape shape, int64_t k, int64_t H,
     const Out *residual, int64_t ld_residual, Out *out) {
     const int tx = 1 << shape.tx_log, lane = threadIdx.x & (tx - 1);
-    const int64_t per = kRowThreads >> shape.tx_log;
+    const int64_t per = kRowThreads >> shape.tx_log, rounds = (shape.T + per - 1) / per;
     const int64_t vecs = (H + 7) / 8;
-    for (int64_t t = blockIdx.x * per + (threadIdx.x >> shape.tx_log); t < shape.T;
-         t += gridDim.x * per) {
-        for (int64_t v = lane; v < vecs; v += tx) {
-            const int n = vec_count(H, v);
+    for (int64_t round = blockIdx.x; round < rounds; round += gridDim.x) {
+        const int64_t own = round * per + (threadIdx.x >> shape.tx_log);
+        const int64_t t = own < shape.T ? own : shape.T - 1;
+        for (int64_t v0 = (int64_t)blockIdx.y * tx; v0 < vecs; v0 += (int64_t)gridDim.y * tx) {
+            const int64_t v = v0 + lane;
+            const Span s = row_span(v, H);
             float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (residual) load8(residual + t * ld_residual + 8 * v, n, acc);
-            for (int64_t j = 0; j < k; ++j) {
-                const int32_t row = slot_row[t * k + j];
-                if (row < 0 || row >= R) continue;
-                const float w = weights ? weights[t * k + j] : 1.0f;
-                float f[8];
-                load8(ys + row * ld + 8 * v, n, f);
+            Raw8<Out> first;
+            zero_raw(first);
+            if (residual)
+                load_raw<kNarrow>(residual + t * ld_residual + s.col, s.hi, first);
+            if (k == 0) unpack(first, acc);
+            for (int64_t j0 = 0; j0 < k; j0 += kBatch) {
+                Batch<kBatch> batch;
+                Raw8<In> raw[kBatch];
+                batch.load(slot_row, weights, t, k, j0);
+                batch.share(k, j0, R);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w, f[i], acc[i]);
+                for (int b = 0; b < kBatch; ++b) {
+                    zero_raw(raw[b]);
+                    if (batch.rows[b] >= 0)
+                        load_raw<kNarrow>(ys + (int64_t)batch.rows[b] * ld + s.col, s.hi, raw[b]);
+                }
+                if (j0 == 0) unpack(first, acc);
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    float f[8];
+                    unpack(raw[b], f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        acc[i] = batch.rows[b] < 0 ? acc[i]
+                                                   : __builtin_fmaf(batch.w[b], f[i], acc[i]);
+                }
             }
-            store8(out + t * H + 8 * v, n, acc);
+            if (own < shape.T && s.any()) store_span(out + t * H, s, acc);
         }
     }
 }
 
-// One token a workgroup: dys rows and the dot products, eight slots at a
-// time (kBatch).
-constexpr int kBatch = 8;
-
-template <typename V>
-__global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(
+// dys rows and the dot products: one token a workgroup, kCount slots at a time.
+template <typename V, int kThreads, int kCount, bool kNarrow>
+__global__ __launch_bounds__(kThreads) void combine_grad_kernel(
     const V *__restrict__ dout, int64_t ld_dout, const V *__restrict__ ys, int64_t ld_ys,
     int64_t R, const int32_t *__restrict__ slot_row, const float *__restrict__ weights,
     int64_t T, int64_t k, int64_t H, V *__restrict__ dys, float *__restrict__ dweights) {
-    __shared__ float part[kRowThreads / 64][kBatch];
+    __shared__ float part[kThreads / 64][kCount];
     const int64_t vecs = (H + 7) / 8;
+    const int waves = blockDim.x / 64;
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-        for (int64_t j0 = 0; j0 < k; j0 += kBatch) {
-            float dot[kBatch] = {0, 0, 0, 0, 0, 0, 0, 0};
-            for (int64_t v = threadIdx.x; v < vecs; v += kRowThreads) {
-                const int n = vec_count(H, v);
-                float d[8];
-                load8(dout + t * ld_dout + 8 * v, n, d);
+        for (int64_t j0 = 0; j0 < k; j0 += kCount) {
+            Batch<kCount> batch;
+            float dot[kCount] = {};
+            batch.load(slot_row, weights, t, k, j0);
+            batch.share(k, j0, R);
+            const int32_t(&rows)[kCount] = batch.rows;
+            const float(&w)[kCount] = batch.w;
+            for (int64_t v = threadIdx.x; v < vecs; v += blockDim.x) {
+                const Span s = row_span(v, H);
+                Raw8<V> raw, y[kCount];
+                load_raw<kNarrow>(dout + t * ld_dout + s.col, s.hi, raw);
+                if (dweights) {
 #pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    if (j0 + b >= k) continue;
-                    const int32_t row = slot_row[t * k + j0 + b];
-                    if (row < 0 || row >= R) continue;
-                    const float w = weights ? weights[t * k + j0 + b] : 1.0f;
-                    float f[8];
-                    if (dweights) {
-                        load8(ys + row * ld_ys + 8 * v, n, f);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) dot[b] = __builtin_fmaf(d[i], f[i], dot[b]);
+                    for (int b = 0; b < kCount; ++b) {
+                        zero_raw(y[b]);
+                        if (rows[b] >= 0)
+                            load_raw<kNarrow>(ys + (int64_t)rows[b] * ld_ys + s.col, s.hi, y[b]);
                     }
-                    if (dys) {
+                }
+                float d[8];
+                unpack_own(raw, s, d);
+                if (dys) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) f[i] = w * d[i];
-                        store8(dys + row * H + 8 * v, n, f);
+                    for (int b = 0; b < kCount; ++b) {
+                        if (rows[b] < 0) continue;
+                        float g[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) g[i] = w[b] * d[i];
+                        store_span(dys + rows[b] * H, s, g);
+                    }
+                }
+                if (dweights) {
+#pragma unroll
+                    for (int b = 0; b < kCount; ++b) {
+                        float f[8];
+                        unpack_own(y[b], s, f);
+                        float sum = 0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(d[i], f[i], sum);
+                        // (a dropped slot has no product, not one with zero)
+                        dot[b] = rows[b] < 0 ? 0.0f : dot[b] + sum;
                     }
                 }
             }
             if (!dweights) continue;
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
+            for (int b = 0; b < kCount; ++b) {
 #pragma unroll
                 for (int m = 32; m; m /= 2) dot[b] += __shfl_xor(dot[b], m);
                 if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6][b] = dot[b];
             }
             __syncthreads();
-            if (threadIdx.x < kBatch && j0 + threadIdx.x < k) {
+            if (threadIdx.x < kCount && j0 + threadIdx.x < k) {
                 float sum = 0;
-                for (int w = 0; w < kRowThreads / 64; ++w) sum += part[w][threadIdx.x];
+                for (int i = 0; i < waves; ++i) sum += part[i][threadIdx.x];
                 dweights[t * k + j0 + threadIdx.x] = sum;
             }
             __syncthreads();
@@ -388,38 +607,116 @@ hipError_t launch_moe_sort(const MoeRouting &r, hipStream_t stream) {
     return r.wide_ids ? sort_typed<int64_t>(r, stream) : sort_typed<int32_t>(r, stream);
 }
 
+namespace {
+
+GatherArgs copy_args(const GatherPlane &rows, const GatherPlane *scales, int64_t k, int64_t R) {
+    GatherArgs a = {};
+    a.rows = rows;
+    if (scales) a.scales = *scales;
+    a.k = k;
+    a.R = R;
+    return a;
+}
+
+GatherArgs quant_args(const void *x, int64_t ldx, int64_t H, int64_t k, void *q, float *scales,
+                      int64_t R) {
+    GatherArgs a = {};
+    a.x = static_cast<const Bf16 *>(x);
+    a.ldx = ldx;
+    a.H = H;
+    a.q = static_cast<uint8_t *>(q);
+    a.q_scales = scales;
+    a.k = k;
+    a.R = R;
+    return a;
+}
+
+// go(Gather<...>{}) for quantizing rows of H values.
+template <typename F>
+auto with_quant(bool pow2, int64_t H, F go) {
+    if (H >= 8)
+        return pow2 ? go(Gather<kQuantPow2, false>{}) : go(Gather<kQuant, false>{});
+    return pow2 ? go(Gather<kQuantPow2, true>{}) : go(Gather<kQuant, true>{});
+}
+
+// Few slots: sort and gather in one launch, a workgroup for each token and
+// stretch of its row.  Each goes through all ids, so beyond kFewSlots the
+// sort's own launches are cheaper.
+template <typename M>
+bool sort_dispatch_few(const MoeRouting &r, const GatherArgs &a, int64_t vecs,
+                       hipStream_t stream) {
+    const int64_t along = (vecs + kRowThreads - 1) / kRowThreads;
+    if (r.T == 0 || r.T * r.k > kFewSlots || along > 65535) return false;
+    const dim3 grid((unsigned)r.T + 1, (unsigned)along);
+    if (r.wide_ids)
+        sort_dispatch_kernel<M, int64_t><<<grid, kRowThreads, 0, stream>>>(
+            a, static_cast<const int64_t *>(r.ids), (int)r.T, (int)r.E, r.offsets, r.slot_row,
+            r.row_slot);
+    else
+        sort_dispatch_kernel<M, int32_t><<<grid, kRowThreads, 0, stream>>>(
+            a, static_cast<const int32_t *>(r.ids), (int)r.T, (int)r.E, r.offsets, r.slot_row,
+            r.row_slot);
+    return true;
+}
+
+}  // namespace
+
 hipError_t launch_moe_dispatch(const GatherPlane &rows, const GatherPlane *scales,
                                const int32_t *slot_row, int64_t T, int64_t k, int64_t R,
                                hipStream_t stream) {
-    const int tx = threads_per_row((rows.bytes + 15) / 16, 16, kRowThreads);
-    const GatherPlane none = {nullptr, nullptr, 0, 0, 0};
-    dispatch_kernel<<<row_blocks(T, tx), kRowThreads, 0, stream>>>(
-        rows, scales ? *scales : none, RowShape{T, log2_of(tx)}, slot_row, k, R);
+    const RowGrid g = row_grid(T, (rows.bytes + 15) / 16, 16);
+    dispatch_kernel<Gather<kCopy, false>><<<g.grid, kRowThreads, 0, stream>>>(copy_args(rows, scales, k, R),
+                                                               g.shape, slot_row);
     return hipGetLastError();
 }
 
 hipError_t launch_moe_dispatch_quant(const void *x, int64_t ldx, int64_t T, int64_t H,
                                      const int32_t *slot_row, int64_t k, void *q, float *scales,
                                      int64_t R, bool pow2, hipStream_t stream) {
-    const int tx = threads_per_row((H + kGroup - 1) / kGroup * 16, 16, kRowThreads);
-    auto *kernel = pow2 ? dispatch_quant_kernel<true> : dispatch_quant_kernel<false>;
-    kernel<<<row_blocks(T, tx), kRowThreads, 0, stream>>>(
-        static_cast<const Bf16 *>(x), ldx, RowShape{T, log2_of(tx)}, H, slot_row, k,
-        static_cast<uint8_t *>(q), scales, R);
+    const RowGrid g = row_grid(T, (H + kGroup - 1) / kGroup * 16, 16);
+    with_quant(pow2, H, [&](auto m) {
+        dispatch_kernel<decltype(m)><<<g.grid, kRowThreads, 0, stream>>>(
+            quant_args(x, ldx, H, k, q, scales, R), g.shape, slot_row);
+    });
     return hipGetLastError();
+}
+
+hipError_t launch_moe_sort_dispatch(const MoeRouting &r, const GatherPlane &rows,
+                                    hipStream_t stream) {
+    const int64_t R = r.T * r.k;
+    if (sort_dispatch_few<Gather<kCopy, false>>(r, copy_args(rows, nullptr, r.k, R), (rows.bytes + 15) / 16,
+                                 stream))
+        return hipGetLastError();
+    const hipError_t e = launch_moe_sort(r, stream);
+    return e != hipSuccess ? e
+                           : launch_moe_dispatch(rows, nullptr, r.slot_row, r.T, r.k, R, stream);
+}
+
+hipError_t launch_moe_sort_dispatch_quant(const MoeRouting &r, const void *x, int64_t ldx,
+                                          int64_t H, void *q, float *scales, bool pow2,
+                                          hipStream_t stream) {
+    const int64_t R = r.T * r.k, vecs = (H + kGroup - 1) / kGroup * 16;
+    const GatherArgs a = quant_args(x, ldx, H, r.k, q, scales, R);
+    if (with_quant(pow2, H,
+                   [&](auto m) { return sort_dispatch_few<decltype(m)>(r, a, vecs, stream); }))
+        return hipGetLastError();
+    const hipError_t e = launch_moe_sort(r, stream);
+    return e != hipSuccess ? e
+                           : launch_moe_dispatch_quant(x, ldx, r.T, H, r.slot_row, r.k, q, scales,
+                                                       R, pow2, stream);
 }
 
 hipError_t launch_moe_combine(const void *ys, bool ys_bf16, int64_t ld, int64_t R,
                               const int32_t *slot_row, const float *weights, int64_t T,
                               int64_t k, int64_t H, const void *residual, int64_t ld_residual,
                               void *out, bool out_bf16, hipStream_t stream) {
-    const int tx = threads_per_row((H + 7) / 8, 16, kRowThreads);
-    const RowShape shape{T, log2_of(tx)};
+    const RowGrid g = row_grid(T, (H + 7) / 8, 16);
     auto go = [&](auto in, auto to) {
         using In = decltype(in);
         using Out = decltype(to);
-        combine_kernel<In, Out><<<row_blocks(T, tx), kRowThreads, 0, stream>>>(
-            static_cast<const In *>(ys), ld, R, slot_row, weights, shape, k, H,
+        auto *kernel = H >= 8 ? combine_kernel<In, Out, false> : combine_kernel<In, Out, true>;
+        kernel<<<g.grid, kRowThreads, 0, stream>>>(
+            static_cast<const In *>(ys), ld, R, slot_row, weights, g.shape, k, H,
             static_cast<const Out *>(residual), ld_residual, static_cast<Out *>(out));
     };
     if (ys_bf16) {
@@ -435,11 +732,17 @@ hipError_t launch_moe_combine_grad(const void *dout, int64_t ld_dout, const void
                                    const float *weights, int64_t T, int64_t k, int64_t H,
                                    void *dys, float *dweights, hipStream_t stream) {
     const unsigned blocks = (unsigned)(T < kMaxBlocks ? T : kMaxBlocks);
+    // Few tokens do not fill the card, so there a row has up to 1024 threads.
+    const bool few = T < 256;
+    const int threads = threads_per_row((H + 7) / 8, 64, few ? 1024 : 256);
     auto go = [&](auto v) {
         using V = decltype(v);
-        combine_grad_kernel<V><<<blocks, kRowThreads, 0, stream>>>(
-            static_cast<const V *>(dout), ld_dout, static_cast<const V *>(ys), ld_ys, R, slot_row,
-            weights, T, k, H, static_cast<V *>(dys), dweights);
+        auto *kernel = H < 8  ? combine_grad_kernel<V, 256, 4, true>
+                       : few  ? combine_grad_kernel<V, 1024, 4, false>
+                              : combine_grad_kernel<V, 256, kBatch, false>;
+        kernel<<<blocks, threads, 0, stream>>>(static_cast<const V *>(dout), ld_dout,
+                                               static_cast<const V *>(ys), ld_ys, R, slot_row,
+                                               weights, T, k, H, static_cast<V *>(dys), dweights);
     };
     if (bf16) go(Bf16{}); else go(float{});
     return hipGetLastError();

@@ -9,7 +9,9 @@
 //
 // About 14 flops a value forward and 30 backward against 7 to 18 bytes: the
 // bound is HBM.  A row stays in the registers of the threads that share it,
-// so each tensor is read and written once; the statistics are FP32 sums.
+// so each tensor is read and written once; a workgroup keeps the parameters
+// of its columns in registers over its rows and has the next row's loads
+// under way while a row's sums are waited for.  The statistics are FP32 sums.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -46,87 +48,129 @@ __device__ __forceinline__ void row_sum(float (&v)[kSums], int tx, float *lds, i
     }
 }
 
-// n values of a parameter row from column 8 v on (ones without one).
-__device__ __forceinline__ void load_param(const void *p, bool bf16, int64_t at, int n,
+// A parameter's values of a span (ones without one).
+template <bool kNarrow>
+__device__ __forceinline__ void load_param(const void *p, bool bf16, int64_t at, const Span &s,
                                            float (&f)[8]) {
     if (!p) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = i < n ? 1.0f : 0.0f;
+        for (int i = 0; i < 8; ++i) f[i] = 1.0f;
     } else if (bf16) {
-        load8(static_cast<const Bf16 *>(p) + at, n, f);
+        Raw8<Bf16> r;
+        load_raw<kNarrow>(static_cast<const Bf16 *>(p) + at + s.col, s.hi, r);
+        unpack(r, f);
     } else {
-        load8(static_cast<const float *>(p) + at, n, f);
+        Raw8<float> r;
+        load_raw<kNarrow>(static_cast<const float *>(p) + at + s.col, s.hi, r);
+        unpack(r, f);
     }
 }
 
-// A thread holds vectors lane, lane + tx, ... (kVecs of them) of its row.
-template <typename Y, typename S, int kVecs, bool kSmall, bool kQuant>
-__global__ void norm_kernel(NormArgs a, int tx, int64_t rows_each) {
+// How a kernel is built: y's and the stream's type, vectors of a row that a
+// thread holds (lane, lane + tx, ...), rows of up to 64 threads (kSmall: many
+// to a workgroup, sums inside a wave) and rows of fewer than eight values.
+template <typename Y_, typename S_, int kVecs_, bool kSmall_, bool kNarrow_>
+struct Build {
+    using Y = Y_;
+    using S = S_;
+    static constexpr int vecs = kVecs_;
+    static constexpr bool small = kSmall_, narrow = kNarrow_;
+    static constexpr int threads = kSmall_ ? kSmallThreads : 1024;
+};
+
+// Which row's threads these are: `member` counts workgroups, or rows' threads.
+template <bool kSmall>
+__device__ __forceinline__ int64_t member_of(int tx) {
+    return kSmall ? blockIdx.x * (int64_t)(kSmallThreads / tx) + threadIdx.x / tx : blockIdx.x;
+}
+
+template <typename B, bool kQuant>
+__global__ __launch_bounds__(B::threads) void norm_kernel(NormArgs a, int tx, int64_t rows_each) {
+    using Y = typename B::Y;
+    using S = typename B::S;
+    constexpr int kVecs = B::vecs;
     __shared__ float lds[2 * 16];
     int turn = 0;
-    const int lane = kSmall ? threadIdx.x & (tx - 1) : threadIdx.x;
-    const int64_t member = kSmall ? blockIdx.x * (int64_t)(kSmallThreads / tx) + threadIdx.x / tx
-                                  : blockIdx.x;
-    const int64_t t0 = member * rows_each;
+    const int lane = B::small ? threadIdx.x & (tx - 1) : threadIdx.x;
+    const int64_t t0 = member_of<B::small>(tx) * rows_each;
+    const int64_t t1 = t0 + rows_each < a.T ? t0 + rows_each : a.T;
+    if (t0 >= t1) return;  // all threads of the row
     const float inv_h = 1.0f / (float)a.H;
-    const int64_t per_gate = a.T / a.gate_rows;
-    for (int64_t t = t0; t < t0 + rows_each; ++t) {
-        if (t >= a.T) {
-            if (kSmall) break;  // the sums stay inside a row's threads
-            return;             // the whole workgroup
+    const int64_t per_gate = a.T / a.gate_rows, G = (a.H + kGroup - 1) / kGroup;
+    const bool want_n = a.n || kQuant;
+
+    Span span[kVecs];
+    Raw8<Y> y_raw[kVecs];
+    Raw8<S> r_raw[kVecs];
+    auto load_row = [&](int64_t t) {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            load_raw<B::narrow>(static_cast<const Y *>(a.y) + t * a.ldy + span[j].col, span[j].hi,
+                                y_raw[j]);
+            load_raw<B::narrow>(static_cast<const S *>(a.r) + t * a.ldr + span[j].col, span[j].hi,
+                                r_raw[j]);
         }
-        float y[kVecs][8], s[kVecs][8], w[8];
+    };
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) span[j] = row_span(lane + (int64_t)j * tx, a.H);
+    load_row(t0);
+    float w_post[kVecs][8], w_pre[kVecs][8], gate[kVecs][8];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+        load_param<B::narrow>(a.post ? a.w_post : nullptr, a.param_bf16, 0, span[j], w_post[j]);
+        load_param<B::narrow>(want_n ? a.w_pre : nullptr, a.param_bf16, 0, span[j], w_pre[j]);
+    }
+    int64_t gate_row = -1;
+    for (int64_t t = t0; t < t1; ++t) {
+        float y[kVecs][8], s[kVecs][8];
         float sum[1] = {0};
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            const int64_t v = lane + (int64_t)j * tx;
-            const int n = vec_count(a.H, v);
-            load8(static_cast<const Y *>(a.y) + t * a.ldy + 8 * v, n, y[j]);
-            load8(static_cast<const S *>(a.r) + t * a.ldr + 8 * v, n, s[j]);
+            unpack_own(y_raw[j], span[j], y[j]);
+            unpack_own(r_raw[j], span[j], s[j]);
+        }
+        if (t + 1 < t1) load_row(t + 1);
+        if (gate_row != t / per_gate) {
+            gate_row = t / per_gate;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(y[j][i], y[j][i], sum[0]);
+            for (int j = 0; j < kVecs; ++j)
+                load_param<B::narrow>(a.gate, a.param_bf16, gate_row * a.H, span[j], gate[j]);
         }
         float rs1 = 1.0f;
         if (a.post) {
-            row_sum<1, kSmall>(sum, tx, lds, turn);
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(y[j][i], y[j][i], sum[0]);
+            row_sum<1, B::small>(sum, tx, lds, turn);
             rs1 = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
             if (a.rstd_post && lane == 0) a.rstd_post[t] = rs1;
         }
         sum[0] = 0;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            const int64_t v = lane + (int64_t)j * tx;
-            const int n = vec_count(a.H, v);
-            if (a.post) {
-                load_param(a.w_post, a.param_bf16, 8 * v, n, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[j][i] = y[j][i] * rs1 * w[i];
-            }
-            load_param(a.gate, a.param_bf16, t / per_gate * a.H + 8 * v, n, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                s[j][i] = a.residual_scale * s[j][i] + a.branch_scale * w[i] * y[j][i];
+                const float u = a.post ? y[j][i] * rs1 * w_post[j][i] : y[j][i];
+                s[j][i] = a.residual_scale * s[j][i] + a.branch_scale * gate[j][i] * u;
                 sum[0] = __builtin_fmaf(s[j][i], s[j][i], sum[0]);
             }
-            store8(static_cast<S *>(a.r_out) + t * a.H + 8 * v, n, s[j]);
+            store_span(static_cast<S *>(a.r_out) + t * a.H, span[j], s[j]);
         }
-        if (!a.n && !kQuant) continue;
-        row_sum<1, kSmall>(sum, tx, lds, turn);
+        if (!want_n) continue;
+        row_sum<1, B::small>(sum, tx, lds, turn);
         const float rs2 = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
         if (a.rstd_pre && lane == 0) a.rstd_pre[t] = rs2;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            const int64_t v = lane + (int64_t)j * tx;
-            const int n = vec_count(a.H, v);
-            load_param(a.w_pre, a.param_bf16, 8 * v, n, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[j][i] = s[j][i] * rs2 * w[i];
-            if (a.n) store8(static_cast<Y *>(a.n) + t * a.H + 8 * v, n, s[j]);
+            for (int i = 0; i < 8; ++i) s[j][i] = s[j][i] * rs2 * w_pre[j][i];
+            if (a.n) store_span(static_cast<Y *>(a.n) + t * a.H, span[j], s[j]);
             if (kQuant) {
-                const int64_t G = (a.H + kGroup - 1) / kGroup;
                 const QuotientCtx qc(row16_max(absmax8(s[j])), a.pow2);
-                store_e4m3(static_cast<uint8_t *>(a.q) + t * a.H + 8 * v, n, quant8(s[j], qc));
-                if ((lane & 15) == 0 && n > 0) a.scales[t * G + v / 16] = qc.s;
+                store_e4m3(static_cast<uint8_t *>(a.q) + t * a.H, span[j], quant8(s[j], qc));
+                if ((lane & 15) == 0 && span[j].any())
+                    a.scales[t * G + (lane + (int64_t)j * tx) / 16] = qc.s;
             }
         }
     }
@@ -138,6 +182,12 @@ __global__ void norm_kernel(NormArgs a, int tx, int64_t rows_each) {
 // in runs that lie within one gate row, or that hold whole gate rows; a
 // member sums its rows' parameter gradients in registers and writes one
 // partial row for each, which a second kernel adds in a fixed order.
+//
+// Both means of a row come from one round of sums: with e = dr', q = b g w1,
+//   c1 = sum A rh / H,  D = e + rs2 (A - rh c1),
+//   c2 = sum q D yh / H = (sum q yh (e + rs2 A) - rs2 c1 sum q yh rh) / H.
+// Within a gate row, dg = b w1 sum D yh and its part of dw1 = b g sum D yh, so
+// one running sum (of D yh) serves both until the gate row ends.
 struct GradPlan {
     int64_t per_gate;   // rows of a gate row
     int64_t run;        // rows of a member
@@ -145,12 +195,10 @@ struct GradPlan {
     int64_t members;
 };
 
-constexpr int64_t kGradMembers = 512;
-
-GradPlan grad_plan(int64_t T, int64_t gate_rows) {
+GradPlan grad_plan(int64_t T, int64_t gate_rows, int64_t most) {
     GradPlan p;
     p.per_gate = T / gate_rows;
-    const int64_t run = (T + kGradMembers - 1) / kGradMembers;
+    const int64_t run = (T + most - 1) / most;
     if (run >= p.per_gate) {
         p.run = run / p.per_gate * p.per_gate;
         p.chunks = 1;
@@ -163,113 +211,150 @@ GradPlan grad_plan(int64_t T, int64_t gate_rows) {
     return p;
 }
 
-template <typename Y, typename S, int kVecs, bool kSmall>
-__global__ void norm_grad_kernel(NormArgs a, GradPlan p, int tx, float *part_post,
-                                 float *part_pre, float *part_gate) {
-    __shared__ float lds[2 * 16];
+template <typename B>
+__global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradPlan p, int tx,
+                                                               float *part_post, float *part_pre,
+                                                               float *part_gate) {
+    using Y = typename B::Y;
+    using S = typename B::S;
+    constexpr int kVecs = B::vecs;
+    __shared__ float lds[2 * 16 * 3];
     int turn = 0;
-    const int lane = kSmall ? threadIdx.x & (tx - 1) : threadIdx.x;
-    const int64_t member = kSmall ? blockIdx.x * (int64_t)(kSmallThreads / tx) + threadIdx.x / tx
-                                  : blockIdx.x;
-    if (member >= p.members) return;
+    const int lane = B::small ? threadIdx.x & (tx - 1) : threadIdx.x;
+    const int64_t member = member_of<B::small>(tx);
+    if (member >= p.members) return;  // all threads of the row
     int64_t t0, t1;
     if (p.chunks == 1) {
         t0 = member * p.run;
-        t1 = t0 + p.run;
-        if (t1 > a.T) t1 = a.T;
+        t1 = t0 + p.run < a.T ? t0 + p.run : a.T;
     } else {
-        const int64_t first = member / p.chunks * p.per_gate;
+        const int64_t first = member / p.chunks * p.per_gate, end = first + p.per_gate;
         t0 = first + member % p.chunks * p.run;
-        t1 = t0 + p.run;
-        if (t1 > first + p.per_gate) t1 = first + p.per_gate;
+        t1 = t0 + p.run < end ? t0 + p.run : end;
     }
     const float inv_h = 1.0f / (float)a.H;
-    float acc1[kVecs][8] = {}, acc2[kVecs][8] = {}, accg[kVecs][8] = {};
-    for (int64_t t = t0; t < t1; ++t) {
-        float d[kVecs][8], rh[kVecs][8], y[kVecs][8], w[8];
-        float sum[1] = {0};
-        const float rs2 = a.dn ? a.in_rstd_pre[t] : 0.0f;
-        const float rs1 = a.post ? a.in_rstd_post[t] : 1.0f;
-        const int64_t grow = t / p.per_gate * a.H;
+
+    Span span[kVecs];
+    Raw8<Y> y_raw[kVecs], dn_raw[kVecs];
+    Raw8<S> r_raw[kVecs], e_raw[kVecs];
+    auto load_row = [&](int64_t t) {
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            const int64_t v = lane + (int64_t)j * tx;
-            const int n = vec_count(a.H, v);
-            load8(static_cast<const Y *>(a.y) + t * a.ldy + 8 * v, n, y[j]);
+            load_raw<B::narrow>(static_cast<const Y *>(a.y) + t * a.ldy + span[j].col, span[j].hi,
+                                y_raw[j]);
             if (a.dn) {
-                load8(static_cast<const Y *>(a.dn) + t * a.ld_dn + 8 * v, n, d[j]);
-                load8(static_cast<const S *>(a.r) + t * a.ldr + 8 * v, n, rh[j]);
-                load_param(a.w_pre, a.param_bf16, 8 * v, n, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    rh[j][i] *= rs2;
-                    acc2[j][i] = __builtin_fmaf(d[j][i], rh[j][i], acc2[j][i]);
-                    d[j][i] *= w[i];
-                    sum[0] = __builtin_fmaf(d[j][i], rh[j][i], sum[0]);
-                }
+                load_raw<B::narrow>(static_cast<const Y *>(a.dn) + t * a.ld_dn + span[j].col,
+                                    span[j].hi, dn_raw[j]);
+                load_raw<B::narrow>(static_cast<const S *>(a.r) + t * a.ldr + span[j].col,
+                                    span[j].hi, r_raw[j]);
             }
+            if (a.dr_out)
+                load_raw<B::narrow>(
+                    static_cast<const S *>(a.dr_out) + t * a.ld_dr_out + span[j].col, span[j].hi,
+                    e_raw[j]);
         }
-        if (a.dn) row_sum<1, kSmall>(sum, tx, lds, turn);
-        const float c1 = sum[0] * inv_h;
-        sum[0] = 0;
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            const int64_t v = lane + (int64_t)j * tx;
-            const int n = vec_count(a.H, v);
-            float e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (a.dr_out) load8(static_cast<const S *>(a.dr_out) + t * a.ld_dr_out + 8 * v, n, e);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                d[j][i] = a.dn ? e[i] + rs2 * (d[j][i] - rh[j][i] * c1) : e[i];
-                e[i] = a.residual_scale * d[j][i];
-            }
-            store8(static_cast<S *>(a.dr) + t * a.H + 8 * v, n, e);
-            load_param(a.gate, a.param_bf16, grow + 8 * v, n, w);
-            float w1[8];
-            load_param(a.post ? a.w_post : nullptr, a.param_bf16, 8 * v, n, w1);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                y[j][i] *= rs1;
-                const float scaled = a.branch_scale * d[j][i];
-                accg[j][i] = __builtin_fmaf(scaled * y[j][i], w1[i], accg[j][i]);
-                const float du = scaled * w[i];
-                acc1[j][i] = __builtin_fmaf(du, y[j][i], acc1[j][i]);
-                d[j][i] = du * w1[i];
-                sum[0] = __builtin_fmaf(d[j][i], y[j][i], sum[0]);
-            }
-        }
-        float c2 = 0;
-        if (a.post) {
-            row_sum<1, kSmall>(sum, tx, lds, turn);
-            c2 = sum[0] * inv_h;
-        }
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            const int64_t v = lane + (int64_t)j * tx;
-            const int n = vec_count(a.H, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) d[j][i] = rs1 * (d[j][i] - y[j][i] * c2);
-            store8(static_cast<Y *>(a.dy) + t * a.H + 8 * v, n, d[j]);
-        }
-        // a gate row that ends here and lies whole in this member
-        if (a.dgate && p.chunks == 1 && (t + 1) % p.per_gate == 0) {
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                const int64_t v = lane + (int64_t)j * tx;
-                store8(a.dgate + grow + 8 * v, vec_count(a.H, v), accg[j]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) accg[j][i] = 0;
-            }
-        }
-    }
+    };
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-        const int64_t v = lane + (int64_t)j * tx;
-        const int n = vec_count(a.H, v);
-        const int64_t at = member * a.H + 8 * v;
-        if (a.dw_post) store8(part_post + at, n, acc1[j]);
-        if (a.dw_pre) store8(part_pre + at, n, acc2[j]);
-        if (a.dgate && p.chunks > 1) store8(part_gate + at, n, accg[j]);
+        span[j] = row_span(lane + (int64_t)j * tx, a.H);
+        zero_raw(dn_raw[j]);
+        zero_raw(r_raw[j]);
+        zero_raw(e_raw[j]);
+    }
+    if (t0 < t1) load_row(t0);
+    // q = b g w1, w2; sums of D yh (this gate row), of its parts of dw1, dw2
+    float q[kVecs][8], w2[kVecs][8];
+    float acc[kVecs][8] = {}, acc1[kVecs][8] = {}, acc2[kVecs][8] = {};
+    const void *post_weights = a.post ? a.w_post : nullptr;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+        load_param<B::narrow>(a.dn ? a.w_pre : nullptr, a.param_bf16, 0, span[j], w2[j]);
+    int64_t gate_row = -1;
+    auto begin_gate_row = [&](int64_t row) {
+        gate_row = row;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            float w1[8];
+            load_param<B::narrow>(post_weights, a.param_bf16, 0, span[j], w1);
+            load_param<B::narrow>(a.gate, a.param_bf16, gate_row * a.H, span[j], q[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[j][i] = a.branch_scale * q[j][i] * w1[i];
+        }
+    };
+    auto end_gate_row = [&] {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            float w[8];
+            load_param<B::narrow>(a.gate, a.param_bf16, gate_row * a.H, span[j], w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                acc[j][i] *= a.branch_scale;
+                acc1[j][i] = __builtin_fmaf(w[i], acc[j][i], acc1[j][i]);
+            }
+            if (a.dgate) {
+                load_param<B::narrow>(post_weights, a.param_bf16, 0, span[j], w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[j][i] *= w[i];
+                store_span(p.chunks == 1 ? a.dgate + gate_row * a.H : part_gate + member * a.H,
+                           span[j], acc[j]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[j][i] = 0;
+        }
+    };
+    for (int64_t t = t0; t < t1; ++t) {
+        const float rs2 = a.dn ? a.in_rstd_pre[t] : 0.0f;
+        const float rs1 = a.post ? a.in_rstd_post[t] : 1.0f;
+        float A[kVecs][8], rh[kVecs][8], yh[kVecs][8], e[kVecs][8];
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            unpack_own(y_raw[j], span[j], yh[j]);
+            unpack_own(dn_raw[j], span[j], A[j]);
+            unpack_own(r_raw[j], span[j], rh[j]);
+            unpack_own(e_raw[j], span[j], e[j]);
+        }
+        if (t + 1 < t1) load_row(t + 1);
+        if (gate_row != t / p.per_gate) {
+            if (gate_row >= 0) end_gate_row();
+            begin_gate_row(t / p.per_gate);
+        }
+        float sum[3] = {0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                yh[j][i] *= rs1;
+                rh[j][i] *= rs2;
+                acc2[j][i] = __builtin_fmaf(A[j][i], rh[j][i], acc2[j][i]);
+                A[j][i] *= w2[j][i];
+                sum[0] = __builtin_fmaf(A[j][i], rh[j][i], sum[0]);
+                e[j][i] = __builtin_fmaf(rs2, A[j][i], e[j][i]);
+                const float qy = q[j][i] * yh[j][i];
+                sum[1] = __builtin_fmaf(qy, e[j][i], sum[1]);
+                sum[2] = __builtin_fmaf(qy, rh[j][i], sum[2]);
+            }
+        row_sum<3, B::small>(sum, tx, lds, turn);
+        const float c1 = rs2 * sum[0] * inv_h;
+        const float c2 = a.post ? (sum[1] - c1 * sum[2]) * inv_h : 0.0f;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            float dr[8], dy[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float D = __builtin_fmaf(-c1, rh[j][i], e[j][i]);
+                dr[i] = a.residual_scale * D;
+                acc[j][i] = __builtin_fmaf(D, yh[j][i], acc[j][i]);
+                dy[i] = rs1 * (D * q[j][i] - yh[j][i] * c2);
+            }
+            store_span(static_cast<S *>(a.dr) + t * a.H, span[j], dr);
+            store_span(static_cast<Y *>(a.dy) + t * a.H, span[j], dy);
+        }
+    }
+    if (gate_row >= 0) end_gate_row();
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+        if (a.dw_post) store_span(part_post + member * a.H, span[j], acc1[j]);
+        if (a.dw_pre) store_span(part_pre + member * a.H, span[j], acc2[j]);
     }
 }
 
@@ -332,25 +417,27 @@ RowSplit row_split(int64_t H) {
     return s;
 }
 
-// Calls f(Y{}, S{}, vecs, small) for the types and split at hand.
-template <int N>
-struct Count {
-    static constexpr int value = N;
-};
-
-template <typename F>
-void with_split(const RowSplit &s, F f) {
-    if (s.small) f(Count<1>{}, Count<1>{});
-    else if (s.vecs == 1) f(Count<1>{}, Count<0>{});
-    else if (s.vecs == 2) f(Count<2>{}, Count<0>{});
-    else f(Count<4>{}, Count<0>{});
+// f(Build<...>{}) for the types and the split at hand.
+template <typename Y, typename S, typename F>
+void with_split(const RowSplit &s, int64_t H, F f) {
+    if (H < 8) f(Build<Y, S, 1, true, true>{});
+    else if (s.small) f(Build<Y, S, 1, true, false>{});
+    else if (s.vecs == 1) f(Build<Y, S, 1, false, false>{});
+    else if (s.vecs == 2) f(Build<Y, S, 2, false, false>{});
+    else f(Build<Y, S, 4, false, false>{});
 }
 
 template <typename F>
-void with_types(const NormArgs &a, F f) {
-    if (a.y_bf16 && a.r_bf16) f(Bf16{}, Bf16{});
-    else if (a.y_bf16) f(Bf16{}, float{});
-    else f(float{}, float{});
+void with_build(const NormArgs &a, const RowSplit &s, F f) {
+    if (a.y_bf16 && a.r_bf16) with_split<Bf16, Bf16>(s, a.H, f);
+    else if (a.y_bf16) with_split<Bf16, float>(s, a.H, f);
+    else with_split<float, float>(s, a.H, f);
+}
+
+// Members that share the rows: enough workgroups to fill the card, as few
+// partial rows as that allows.
+int64_t grad_members(const RowSplit &s) {
+    return s.small ? 512 * (kSmallThreads / s.tx) : s.block >= 512 ? 512 : 1024;
 }
 
 }  // namespace
@@ -359,52 +446,38 @@ hipError_t launch_norm_residual(const NormArgs &a, hipStream_t stream) {
     const RowSplit s = row_split(a.H);
     const int64_t per = s.small ? kSmallThreads / s.tx : 1;
     int64_t blocks = (a.T + per - 1) / per;
-    const int64_t most = 2048;
+    const int64_t most = s.block >= 512 ? 512 : 2048;
     int64_t rows_each = 1;
     if (blocks > most) {
         rows_each = (a.T + most * per - 1) / (most * per);
         blocks = (a.T + rows_each * per - 1) / (rows_each * per);
     }
-    with_types(a, [&](auto y, auto r) {
-        with_split(s, [&](auto vecs, auto small) {
-            using Y = decltype(y);
-            using S = decltype(r);
-            constexpr int V = decltype(vecs)::value;
-            constexpr bool kSmall = decltype(small)::value;
-            if (a.q)
-                norm_kernel<Y, S, V, kSmall, true>
-                    <<<(unsigned)blocks, s.block, 0, stream>>>(a, s.tx, rows_each);
-            else
-                norm_kernel<Y, S, V, kSmall, false>
-                    <<<(unsigned)blocks, s.block, 0, stream>>>(a, s.tx, rows_each);
-        });
+    with_build(a, s, [&](auto b) {
+        using B = decltype(b);
+        auto *kernel = a.q ? norm_kernel<B, true> : norm_kernel<B, false>;
+        kernel<<<(unsigned)blocks, s.block, 0, stream>>>(a, s.tx, rows_each);
     });
     return hipGetLastError();
 }
 
 size_t norm_grad_workspace_bytes(int64_t T, int64_t H, int64_t gate_rows) {
-    if (T == 0) return 0;
-    const GradPlan p = grad_plan(T, gate_rows);
+    if (T == 0 || H == 0) return 0;
+    const GradPlan p = grad_plan(T, gate_rows, grad_members(row_split(H)));
     return (size_t)(p.chunks > 1 ? 3 : 2) * p.members * H * sizeof(float);
 }
 
 hipError_t launch_norm_residual_grad(const NormArgs &a, hipStream_t stream) {
+    const RowSplit s = row_split(a.H);
     GradPlan p = {1, 1, 1, 0};
-    if (a.T > 0) p = grad_plan(a.T, a.gate_rows);
+    if (a.T > 0) p = grad_plan(a.T, a.gate_rows, grad_members(s));
     float *part_post = a.workspace, *part_pre = part_post + p.members * a.H;
     float *part_gate = part_pre + p.members * a.H;
     if (a.T > 0) {
-        const RowSplit s = row_split(a.H);
         const int64_t per = s.small ? kSmallThreads / s.tx : 1;
         const int64_t blocks = (p.members + per - 1) / per;
-        with_types(a, [&](auto y, auto r) {
-            with_split(s, [&](auto vecs, auto small) {
-                using Y = decltype(y);
-                using S = decltype(r);
-                norm_grad_kernel<Y, S, decltype(vecs)::value, decltype(small)::value>
-                    <<<(unsigned)blocks, s.block, 0, stream>>>(a, p, s.tx, part_post, part_pre,
-                                                               part_gate);
-            });
+        with_build(a, s, [&](auto b) {
+            norm_grad_kernel<decltype(b)><<<(unsigned)blocks, s.block, 0, stream>>>(
+                a, p, s.tx, part_post, part_pre, part_gate);
         });
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;

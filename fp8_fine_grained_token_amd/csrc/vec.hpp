@@ -1,8 +1,11 @@
 // Eight values of a row at a time, from bf16 or fp32 rows of any alignment.
 //
-// gfx950 reads and writes 16 bytes at any byte address, so a row of odd
-// width needs no scalar path: only the last vector of a row (n < 8 values)
-// is taken value by value.
+// gfx950 reads and writes 16 bytes at any byte address, so a row of odd width
+// or alignment needs no scalar path.  The last vector of a row is read as the
+// row's last eight values (some of them its neighbour's): a load is then the
+// same for every lane, and nothing but a store depends on where a row ends.
+// Loads keep what they read as it is (Raw8) until it is used, so that many
+// can be under way.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -12,6 +15,7 @@
 
 namespace fp8blk {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 typedef uint32_t u32_any __attribute__((aligned(1)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
@@ -34,77 +38,129 @@ __device__ __forceinline__ float to_float(Bf16 v) {
 __device__ __forceinline__ void from_float(float f, float &v) { v = f; }
 __device__ __forceinline__ void from_float(float f, Bf16 &v) { v.bits = (uint16_t)to_bf16(f); }
 
-// n in [0, 8] values at p, zeros past them.
-__device__ __forceinline__ void load8(const Bf16 *p, int n, float (&f)[8]) {
-    if (n == 8) {
-        const u32x4_any v = *reinterpret_cast<const u32x4_any *>(p);
-        unpack8(make_uint4(v.x, v.y, v.z, v.w), f);
+// Vector v of a row of H values: values col .. col + 7, of which those from
+// index lo up to hi are its own (none past the last vector; hi < 8 only in
+// rows of fewer than eight values).
+struct Span {
+    int64_t col;
+    int lo, hi;
+    __device__ __forceinline__ bool whole() const { return lo == 0 && hi == 8; }
+    __device__ __forceinline__ bool any() const { return lo < hi; }
+    __device__ __forceinline__ bool has(int i) const { return i >= lo && i < hi; }
+};
+
+__device__ __forceinline__ Span row_span(int64_t v, int64_t H) {
+    Span s;
+    s.hi = H < 8 ? (int)H : 8;
+    s.col = 8 * v < H - s.hi ? 8 * v : H - s.hi;
+    const int64_t over = 8 * v - s.col;
+    s.lo = over < 8 ? (int)over : 8;
+    return s;
+}
+
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<Bf16> {
+    u32x4 v;
+};
+template <>
+struct Raw8<float> {
+    u32x4 a, b;
+};
+
+// The eight values from p on; in rows of fewer than eight (kNarrow) those
+// there are, the last one repeated.  A template parameter: as a branch it
+// would put a wait after every load.
+template <bool kNarrow>
+__device__ __forceinline__ void load_raw(const Bf16 *p, int hi, Raw8<Bf16> &r) {
+    if (!kNarrow) {
+        r.v = *reinterpret_cast<const u32x4_any *>(p);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = i < n ? to_float(p[i]) : 0.0f;
+        for (int i = 0; i < 4; ++i)
+            r.v[i] = p[min(2 * i, hi - 1)].bits | (uint32_t)p[min(2 * i + 1, hi - 1)].bits << 16;
     }
 }
-__device__ __forceinline__ void load8(const float *p, int n, float (&f)[8]) {
-    if (n == 8) {
-        const u32x4_any a = *reinterpret_cast<const u32x4_any *>(p);
-        const u32x4_any b = *reinterpret_cast<const u32x4_any *>(p + 4);
-        f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y);
-        f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
-        f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y);
-        f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+template <bool kNarrow>
+__device__ __forceinline__ void load_raw(const float *p, int hi, Raw8<float> &r) {
+    if (!kNarrow) {
+        r.a = *reinterpret_cast<const u32x4_any *>(p);
+        r.b = *reinterpret_cast<const u32x4_any *>(p + 4);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = i < n ? p[i] : 0.0f;
+        for (int i = 0; i < 4; ++i) {
+            r.a[i] = __float_as_uint(p[min(i, hi - 1)]);
+            r.b[i] = __float_as_uint(p[min(i + 4, hi - 1)]);
+        }
     }
 }
-__device__ __forceinline__ void store8(Bf16 *p, int n, const float (&f)[8]) {
-    if (n == 8) {
+__device__ __forceinline__ void zero_raw(Raw8<Bf16> &r) { r.v = u32x4{0, 0, 0, 0}; }
+__device__ __forceinline__ void zero_raw(Raw8<float> &r) { r.a = r.b = u32x4{0, 0, 0, 0}; }
+
+__device__ __forceinline__ void unpack(const Raw8<Bf16> &r, float (&f)[8]) {
+    unpack8(make_uint4(r.v.x, r.v.y, r.v.z, r.v.w), f);
+}
+__device__ __forceinline__ void unpack(const Raw8<float> &r, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[i] = __uint_as_float(r.a[i]);
+        f[i + 4] = __uint_as_float(r.b[i]);
+    }
+}
+// The span's own values, zeros for the others.
+template <typename T>
+__device__ __forceinline__ void unpack_own(const Raw8<T> &r, const Span &s, float (&f)[8]) {
+    unpack(r, f);
+    if (!s.whole()) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = s.has(i) ? f[i] : 0.0f;
+    }
+}
+
+// The span's own values to a row.
+__device__ __forceinline__ void store_span(Bf16 *row, const Span &s, const float (&f)[8]) {
+    if (s.whole()) {
         u32x4_any v;
         v.x = to_bf16(f[0]) | (to_bf16(f[1]) << 16);
         v.y = to_bf16(f[2]) | (to_bf16(f[3]) << 16);
         v.z = to_bf16(f[4]) | (to_bf16(f[5]) << 16);
         v.w = to_bf16(f[6]) | (to_bf16(f[7]) << 16);
-        *reinterpret_cast<u32x4_any *>(p) = v;
+        *reinterpret_cast<u32x4_any *>(row + s.col) = v;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) from_float(f[i], p[i]);
+            if (s.has(i)) from_float(f[i], row[s.col + i]);
     }
 }
-__device__ __forceinline__ void store8(float *p, int n, const float (&f)[8]) {
-    if (n == 8) {
+__device__ __forceinline__ void store_span(float *row, const Span &s, const float (&f)[8]) {
+    if (s.whole()) {
         u32x4_any a, b;
         a.x = __float_as_uint(f[0]); a.y = __float_as_uint(f[1]);
         a.z = __float_as_uint(f[2]); a.w = __float_as_uint(f[3]);
         b.x = __float_as_uint(f[4]); b.y = __float_as_uint(f[5]);
         b.z = __float_as_uint(f[6]); b.w = __float_as_uint(f[7]);
-        *reinterpret_cast<u32x4_any *>(p) = a;
-        *reinterpret_cast<u32x4_any *>(p + 4) = b;
+        *reinterpret_cast<u32x4_any *>(row + s.col) = a;
+        *reinterpret_cast<u32x4_any *>(row + s.col + 4) = b;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = f[i];
+            if (s.has(i)) row[s.col + i] = f[i];
     }
 }
-
-// E4M3 bytes of one lane's n values of a 1x128 group.
-__device__ __forceinline__ void store_e4m3(uint8_t *p, int n, uint2 v) {
-    if (n == 8) {
+// E4M3 bytes of the span's values of a 1x128 group.
+__device__ __forceinline__ void store_e4m3(uint8_t *row, const Span &s, uint2 v) {
+    if (s.whole()) {
         u32x2_any w;
         w.x = v.x;
         w.y = v.y;
-        *reinterpret_cast<u32x2_any *>(p) = w;
+        *reinterpret_cast<u32x2_any *>(row + s.col) = w;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = (uint8_t)((i < 4 ? v.x >> (8 * i) : v.y >> (8 * (i - 4))) & 0xFF);
+            if (s.has(i))
+                row[s.col + i] = (uint8_t)((i < 4 ? v.x >> (8 * i) : v.y >> (8 * (i - 4))) & 0xFF);
     }
-}
-
-// Values of a row that the 8-value vector v holds: min(8, H - 8 v), at least 0.
-__device__ __forceinline__ int vec_count(int64_t H, int64_t v) {
-    const int64_t left = H - 8 * v;
-    return left >= 8 ? 8 : left > 0 ? (int)left : 0;
 }
 
 // The number of threads that share a row of `vecs` vectors: a power of two

@@ -109,7 +109,6 @@ __global__ __launch_bounds__(256) void w4_quant_kernel(const uint16_t *__restric
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 8;
 constexpr int kBlockK = 128;  // channels of a block
