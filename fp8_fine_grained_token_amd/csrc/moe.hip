@@ -31,11 +31,12 @@ namespace {
 // sort is stable and the same in every run.
 constexpr int kSortWaves = 8;
 constexpr int kSortThreads = 64 * kSortWaves;
-constexpr int kSortChunk = 4096;      // slots of a workgroup
+constexpr int kSortHeld = 4;  // slots a lane holds at a time
+constexpr int kSortChunk = kSortThreads * kSortHeld;  // slots of a workgroup
 constexpr int64_t kSortMaxRuns = 512;  // more slots: longer runs
 
 struct SortPlan {
-    int64_t slots, run;  // run: slots of a workgroup, a multiple of kSortThreads
+    int64_t slots, run;  // run: slots of a workgroup, a multiple of kSortChunk
     int runs;
 };
 
@@ -45,7 +46,7 @@ SortPlan sort_plan(int64_t slots) {
     int64_t run = kSortChunk;
     if (slots > run * kSortMaxRuns) {
         run = (slots + kSortMaxRuns - 1) / kSortMaxRuns;
-        run = (run + kSortThreads - 1) / kSortThreads * kSortThreads;
+        run = (run + kSortChunk - 1) / kSortChunk * kSortChunk;
     }
     p.run = run;
     p.runs = (int)((slots + run - 1) / run);
@@ -59,13 +60,34 @@ __device__ __forceinline__ int expert_of(const Id *ids, int64_t slot, int E) {
     return v >= 0 && v < (Id)E ? (int)v : -1;
 }
 
-// Counts of this workgroup's slots, per wave and expert.
+// The experts of the kSortHeld * 64 slots from s0 on, 64 slots to each of a
+// lane's values (-1 past `last` and for dropped slots); one wait for all.
+template <typename Id>
+__device__ __forceinline__ void hold_ids(const Id *ids, int64_t s0, int64_t last, int E,
+                                         int (&e)[kSortHeld]) {
+    Id v[kSortHeld];
+#pragma unroll
+    for (int i = 0; i < kSortHeld; ++i) {
+        const int64_t s = s0 + 64 * i + (threadIdx.x & 63);
+        v[i] = ids[s < last ? s : last - 1];
+    }
+#pragma unroll
+    for (int i = 0; i < kSortHeld; ++i) {
+        const int64_t s = s0 + 64 * i + (threadIdx.x & 63);
+        e[i] = s < last && v[i] >= 0 && v[i] < (Id)E ? (int)v[i] : -1;
+    }
+}
+
+// Adds a wave's slots to counts per expert.
 template <typename Id>
 __device__ __forceinline__ void count_run(const Id *ids, int64_t first, int64_t last, int E,
-                                          int32_t *mine) {
-    for (int64_t s = first + (threadIdx.x & 63); s < last; s += 64) {
-        const int e = expert_of(ids, s, E);
-        if (e >= 0) atomicAdd(&mine[e], 1);
+                                          int32_t *counts) {
+    for (int64_t s0 = first; s0 < last; s0 += 64 * kSortHeld) {
+        int e[kSortHeld];
+        hold_ids(ids, s0, last, E, e);
+#pragma unroll
+        for (int i = 0; i < kSortHeld; ++i)
+            if (e[i] >= 0) atomicAdd(&counts[e[i]], 1);
     }
 }
 
@@ -114,10 +136,11 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(
             if (p.runs == 1) {
                 for (int w = 0; w < kSortWaves; ++w) all[i] += base[w * E + e];
             } else {
+#pragma unroll 8
                 for (int b = 0; b < p.runs; ++b) {
                     const int32_t c = counts[(int64_t)b * E + e];
                     all[i] += c;
-                    if (b < (int)blockIdx.x) before[i] += c;
+                    before[i] += b < (int)blockIdx.x ? c : 0;
                 }
             }
         }
@@ -156,25 +179,30 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(
     int bits = 0;
     while ((1 << bits) < E) ++bits;
     int32_t *mine = base + wave * E;
-    for (int64_t s0 = first; s0 < last; s0 += 64) {
-        const int64_t s = s0 + lane;
-        const int e = s < last ? expert_of(ids, s, E) : -1;
-        uint64_t same = __ballot(e >= 0);
-        for (int b = 0; b < bits; ++b) {
-            const bool set = (e >> b) & 1;
-            const uint64_t with = __ballot(set);
-            same &= set ? with : ~with;
+    for (int64_t s0 = first; s0 < last; s0 += 64 * kSortHeld) {
+        int held[kSortHeld];
+        hold_ids(ids, s0, last, E, held);
+#pragma unroll
+        for (int i = 0; i < kSortHeld; ++i) {
+            const int e = held[i];
+            const int64_t s = s0 + 64 * i + lane;
+            uint64_t same = __ballot(e >= 0);
+            for (int b = 0; b < bits; ++b) {
+                const bool set = (e >> b) & 1;
+                const uint64_t with = __ballot(set);
+                same &= set ? with : ~with;
+            }
+            int32_t row = -1;
+            if (e >= 0) {
+                const int rank = __popcll(same & ((1ull << lane) - 1));
+                const int leader = __ffsll((unsigned long long)same) - 1;
+                int32_t old = 0;
+                if (lane == leader) old = atomicAdd(&mine[e], (int32_t)__popcll(same));
+                row = __shfl(old, leader) + rank;
+                row_slot[row] = (int32_t)s;
+            }
+            if (s < last) slot_row[s] = row;
         }
-        int32_t row = -1;
-        if (e >= 0) {
-            const int rank = __popcll(same & ((1ull << lane) - 1));
-            const int leader = __ffsll((unsigned long long)same) - 1;
-            int32_t old = 0;
-            if (lane == leader) old = atomicAdd(&mine[e], (int32_t)__popcll(same));
-            row = __shfl(old, leader) + rank;
-            row_slot[row] = (int32_t)s;
-        }
-        if (s < last) slot_row[s] = row;
     }
     // rows past the kept slots
     const int64_t end = ((int64_t)blockIdx.x + 1) * p.run;
@@ -377,7 +405,7 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(GatherArgs a, Row
 // all ids (kFewSlots of them are 32 KiB from L2), so there is no launch
 // between the sort and the gather and nothing to wait for.  One more row of
 // workgroups writes the offsets.
-constexpr int64_t kFewSlots = 4096;
+constexpr int64_t kFewSlots = 2048;
 
 template <typename M, typename Id>
 __global__ __launch_bounds__(kRowThreads) void sort_dispatch_kernel(
@@ -429,7 +457,7 @@ __global__ __launch_bounds__(kRowThreads) void sort_dispatch_kernel(
     }
     const int t = blockIdx.x;
     auto get = [&](int64_t j0, int32_t(&rows)[kBatch]) {
-        // key (expert, slot): below 1024 * 4096
+        // key (expert, slot): below 1024 * 2048
         int key[kBatch], count[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {

@@ -120,7 +120,7 @@ __global__ __launch_bounds__(B::threads) void norm_kernel(NormArgs a, int tx, in
         load_param<B::narrow>(a.post ? a.w_post : nullptr, a.param_bf16, 0, span[j], w_post[j]);
         load_param<B::narrow>(want_n ? a.w_pre : nullptr, a.param_bf16, 0, span[j], w_pre[j]);
     }
-    int64_t gate_row = -1;
+    int64_t gate_row = t0 / per_gate - 1, gate_end = (gate_row + 1) * per_gate;
     for (int64_t t = t0; t < t1; ++t) {
         float y[kVecs][8], s[kVecs][8];
         float sum[1] = {0};
@@ -130,8 +130,9 @@ __global__ __launch_bounds__(B::threads) void norm_kernel(NormArgs a, int tx, in
             unpack_own(r_raw[j], span[j], s[j]);
         }
         if (t + 1 < t1) load_row(t + 1);
-        if (gate_row != t / per_gate) {
-            gate_row = t / per_gate;
+        if (t == gate_end || t == t0) {
+            ++gate_row;
+            gate_end = (gate_row + 1) * per_gate;
 #pragma unroll
             for (int j = 0; j < kVecs; ++j)
                 load_param<B::narrow>(a.gate, a.param_bf16, gate_row * a.H, span[j], gate[j]);
@@ -236,8 +237,11 @@ __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradP
 
     Span span[kVecs];
     Raw8<Y> y_raw[kVecs], dn_raw[kVecs];
+    float rs1_next = 1.0f, rs2_next = 0.0f;  // (read with the row: behind the stores they would wait for them)
     Raw8<S> r_raw[kVecs], e_raw[kVecs];
     auto load_row = [&](int64_t t) {
+        if (a.dn) rs2_next = a.in_rstd_pre[t];
+        if (a.post) rs1_next = a.in_rstd_post[t];
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
             load_raw<B::narrow>(static_cast<const Y *>(a.y) + t * a.ldy + span[j].col, span[j].hi,
@@ -262,16 +266,19 @@ __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradP
         zero_raw(e_raw[j]);
     }
     if (t0 < t1) load_row(t0);
-    // q = b g w1, w2; sums of D yh (this gate row), of its parts of dw1, dw2
+    // q = b g w1, w2; sums of D yh (this gate row) and of dw2's terms; the
+    // member's part of dw1 grows in its partial row, once a gate row
     float q[kVecs][8], w2[kVecs][8];
-    float acc[kVecs][8] = {}, acc1[kVecs][8] = {}, acc2[kVecs][8] = {};
+    float acc[kVecs][8] = {}, acc2[kVecs][8] = {};
     const void *post_weights = a.post ? a.w_post : nullptr;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j)
         load_param<B::narrow>(a.dn ? a.w_pre : nullptr, a.param_bf16, 0, span[j], w2[j]);
-    int64_t gate_row = -1;
+    int64_t gate_row = 0, gate_end = 0;
+    bool first_gate = true;
     auto begin_gate_row = [&](int64_t row) {
         gate_row = row;
+        gate_end = (row + 1) * p.per_gate;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
             float w1[8];
@@ -287,9 +294,17 @@ __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradP
             float w[8];
             load_param<B::narrow>(a.gate, a.param_bf16, gate_row * a.H, span[j], w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                acc[j][i] *= a.branch_scale;
-                acc1[j][i] = __builtin_fmaf(w[i], acc[j][i], acc1[j][i]);
+            for (int i = 0; i < 8; ++i) acc[j][i] *= a.branch_scale;
+            if (a.dw_post) {
+                float *part = part_post + member * a.H, sum[8] = {};
+                if (!first_gate) {
+                    Raw8<float> r;
+                    load_raw<B::narrow>(part + span[j].col, span[j].hi, r);
+                    unpack(r, sum);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(w[i], acc[j][i], sum[i]);
+                store_span(part, span[j], sum);
             }
             if (a.dgate) {
                 load_param<B::narrow>(post_weights, a.param_bf16, 0, span[j], w);
@@ -301,10 +316,11 @@ __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradP
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[j][i] = 0;
         }
+        first_gate = false;
     };
+    if (t0 < t1) begin_gate_row(t0 / p.per_gate);
     for (int64_t t = t0; t < t1; ++t) {
-        const float rs2 = a.dn ? a.in_rstd_pre[t] : 0.0f;
-        const float rs1 = a.post ? a.in_rstd_post[t] : 1.0f;
+        const float rs1 = rs1_next, rs2 = rs2_next;
         float A[kVecs][8], rh[kVecs][8], yh[kVecs][8], e[kVecs][8];
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
@@ -314,9 +330,9 @@ __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradP
             unpack_own(e_raw[j], span[j], e[j]);
         }
         if (t + 1 < t1) load_row(t + 1);
-        if (gate_row != t / p.per_gate) {
-            if (gate_row >= 0) end_gate_row();
-            begin_gate_row(t / p.per_gate);
+        if (t == gate_end) {
+            end_gate_row();
+            begin_gate_row(gate_row + 1);
         }
         float sum[3] = {0, 0, 0};
 #pragma unroll
@@ -350,12 +366,10 @@ __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradP
             store_span(static_cast<Y *>(a.dy) + t * a.H, span[j], dy);
         }
     }
-    if (gate_row >= 0) end_gate_row();
+    end_gate_row();
+    if (a.dw_pre)
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-        if (a.dw_post) store_span(part_post + member * a.H, span[j], acc1[j]);
-        if (a.dw_pre) store_span(part_pre + member * a.H, span[j], acc2[j]);
-    }
+        for (int j = 0; j < kVecs; ++j) store_span(part_pre + member * a.H, span[j], acc2[j]);
 }
 
 // out[group][h] = sum over the group's `rows` partial rows: 64 columns a
