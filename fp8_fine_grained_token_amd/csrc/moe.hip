@@ -233,9 +233,15 @@ hipError_t sort_typed(const MoeRouting &r, hipStream_t stream) {
 // to a workgroup, the workgroups of gridDim.y side by side along wide rows.
 // A token's slots are read kBatch at a time, the row numbers of a batch in
 // one go and then the rows, so that a wait covers a batch and not a slot.
+// Where that leaves a thread with one or two loads (the gather reads a row
+// once; few slots a token), it takes four vectors at a time, unless there are
+// too few rows to give every thread work (kManyVecs).
 constexpr int kRowThreads = 256;
 constexpr int kBatch = 8;
 constexpr int64_t kMaxBlocks = (int64_t)1 << 22;
+// Vectors over which a thread takes four: 8192 rows of 7168 values once each,
+// quantized gather 63 -> 44 us, weighted sum 99 -> 50 us.
+constexpr int64_t kManyVecs = (int64_t)1 << 19;
 
 struct RowShape {
     int64_t T;
@@ -254,10 +260,10 @@ struct RowGrid {
     dim3 grid;
 };
 
-RowGrid row_grid(int64_t T, int64_t vecs, int least) {
-    const int tx = threads_per_row(vecs, least, kRowThreads);
+RowGrid row_grid(int64_t T, int64_t vecs, int least, int each = 1) {
+    const int tx = threads_per_row((vecs + each - 1) / each, least, kRowThreads);
     const int64_t per = kRowThreads / tx, blocks = (T + per - 1) / per;
-    const int64_t along = (vecs + tx - 1) / tx;
+    const int64_t along = (vecs + tx * each - 1) / (tx * each);
     RowGrid g;
     g.shape = {T, log2_of(tx)};
     g.grid = dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks),
@@ -297,10 +303,12 @@ struct Batch {
 
 enum GatherMode { kCopy, kQuant, kQuantPow2 };
 
-// Quantizing rows of fewer than eight values or more (a copy does not ask).
-template <int kMode, bool kNarrow>
+// Quantizing rows of fewer than eight values or more (a copy does not ask),
+// vectors a thread takes at a time.
+template <int kMode, bool kNarrow, int kVecs>
 struct Gather {
     static constexpr bool copy = kMode == kCopy, pow2 = kMode == kQuantPow2, narrow = kNarrow;
+    static constexpr int vecs = kVecs;
 };
 
 struct GatherArgs {
@@ -314,56 +322,80 @@ struct GatherArgs {
 
 __device__ __forceinline__ int64_t plane_vecs(const GatherPlane &g) { return (g.bytes + 15) / 16; }
 
-// Bytes 16 v .. of token t's row to the rows of its slots (the row's last 16
-// bytes for its last vector); get(j0, rows) gives a batch of them.
-template <typename Rows>
-__device__ __forceinline__ void copy_vec(const GatherPlane &g, int64_t t, int64_t v, bool in,
-                                         int64_t k, Rows get) {
+// Vectors v, v + step, ... of token t's row (16 bytes, the row's last 16 for
+// its last vector) to the rows of its slots; get(j0, rows) gives a batch of
+// them.
+template <int kVecs, typename Rows>
+__device__ __forceinline__ void copy_vecs(const GatherPlane &g, int64_t t, int64_t v, int64_t step,
+                                          bool in, int64_t k, Rows get) {
     const bool wide = g.bytes >= 16;
-    in = in && 16 * v < g.bytes;
-    const int64_t at = wide ? (16 * v < g.bytes - 16 ? 16 * v : g.bytes - 16) : 0;
-    const uint8_t *src = static_cast<const uint8_t *>(g.src) + t * g.ld + at;
-    uint8_t *dst = static_cast<uint8_t *>(g.dst) + at;
-    u32x4_any d = {0, 0, 0, 0};
-    if (wide) d = *reinterpret_cast<const u32x4_any *>(src);
+    const uint8_t *src = static_cast<const uint8_t *>(g.src) + t * g.ld;
+    int64_t at[kVecs];
+    u32x4 d[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        const int64_t from = 16 * (v + i * step), most = g.bytes - 16;
+        at[i] = !wide ? 0 : from < most ? from : most;
+        d[i] = u32x4{0, 0, 0, 0};
+        if (wide) d[i] = *reinterpret_cast<const u32x4_any *>(src + at[i]);
+    }
     for (int64_t j0 = 0; j0 < k; j0 += kBatch) {
         int32_t rows[kBatch];
         get(j0, rows);
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             if (rows[b] < 0 || !in) continue;
-            if (wide) {
-                *reinterpret_cast<u32x4_any *>(dst + rows[b] * g.bytes) = d;
-            } else {
-                for (int i = 0; i < (int)g.bytes; ++i) dst[rows[b] * g.bytes + i] = src[i];
+            uint8_t *dst = static_cast<uint8_t *>(g.dst) + rows[b] * g.bytes;
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                if (16 * (v + i * step) >= g.bytes) continue;
+                if (wide) {
+                    *reinterpret_cast<u32x4_any *>(dst + at[i]) = d[i];
+                } else {
+                    for (int c = 0; c < (int)g.bytes; ++c) dst[c] = src[c];
+                }
             }
         }
     }
 }
 
-// Vector v of token t quantized (16 lanes hold one 128-value group, eight
-// values each, as in the activation quantizer), for all lanes of a wave or
-// none: the 16-lane maximum needs its lanes.
-template <bool kPow2, bool kNarrow, typename Rows>
-__device__ __forceinline__ void quant_vec(const GatherArgs &a, int64_t t, int64_t v, bool in,
-                                          Rows get) {
+// The same quantized: 16 lanes hold one 128-value group, eight values each, as
+// in the activation quantizer.  For all lanes of a wave or none: the 16-lane
+// maximum needs its lanes.
+template <typename M, typename Rows>
+__device__ __forceinline__ void quant_vecs(const GatherArgs &a, int64_t t, int64_t v, int64_t step,
+                                           bool in, Rows get) {
     const int64_t G = (a.H + kGroup - 1) / kGroup;
-    const Span s = row_span(v, a.H);
-    Raw8<Bf16> raw;
-    load_raw<kNarrow>(a.x + t * a.ldx + s.col, s.hi, raw);
-    float f[8];
-    unpack_own(raw, s, f);
-    const QuotientCtx qc(row16_max(absmax8(f)), kPow2);
-    const uint2 bytes = quant8(f, qc);
-    in = in && s.any();
+    Span s[M::vecs];
+    Raw8<Bf16> raw[M::vecs];
+    uint2 bytes[M::vecs];
+    float scale[M::vecs];
+#pragma unroll
+    for (int i = 0; i < M::vecs; ++i) {
+        s[i] = row_span(v + i * step, a.H);
+        load_raw<M::narrow>(a.x + t * a.ldx + s[i].col, s[i].hi, raw[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < M::vecs; ++i) {
+        float f[8];
+        unpack_own(raw[i], s[i], f);
+        const QuotientCtx qc(row16_max(absmax8(f)), M::pow2);
+        bytes[i] = quant8(f, qc);
+        scale[i] = qc.s;
+    }
     for (int64_t j0 = 0; j0 < a.k; j0 += kBatch) {
         int32_t rows[kBatch];
         get(j0, rows);
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             if (rows[b] < 0 || !in) continue;
-            store_e4m3(a.q + rows[b] * a.H, s, bytes);
-            if ((threadIdx.x & 15) == 0) a.q_scales[rows[b] * G + v / 16] = qc.s;
+#pragma unroll
+            for (int i = 0; i < M::vecs; ++i) {
+                if (!s[i].any()) continue;
+                store_e4m3(a.q + rows[b] * a.H, s[i], bytes[i]);
+                if ((threadIdx.x & 15) == 0)
+                    a.q_scales[rows[b] * G + (v + i * step) / 16] = scale[i];
+            }
         }
     }
 }
@@ -384,17 +416,18 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(GatherArgs a, Row
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) rows[i] = batch.rows[i];
         };
-        const int64_t v0 = (int64_t)blockIdx.y * tx, step = (int64_t)gridDim.y * tx;
         // every lane stays to the end: lanes hand each other row numbers
+        const int64_t v0 = (int64_t)blockIdx.y * tx * M::vecs;
+        const int64_t step = (int64_t)gridDim.y * tx * M::vecs;
         if (M::copy) {
             for (int64_t v = v0; v < plane_vecs(a.rows); v += step)
-                copy_vec(a.rows, t, v + lane, in, a.k, get);
+                copy_vecs<M::vecs>(a.rows, t, v + lane, tx, in, a.k, get);
             if (a.scales.src)
                 for (int64_t v = v0; v < plane_vecs(a.scales); v += step)
-                    copy_vec(a.scales, t, v + lane, in, a.k, get);
+                    copy_vecs<M::vecs>(a.scales, t, v + lane, tx, in, a.k, get);
         } else {
             for (int64_t v = v0; v < 16 * ((a.H + kGroup - 1) / kGroup); v += step)
-                quant_vec<M::pow2, M::narrow>(a, t, v + lane, in, get);
+                quant_vecs<M>(a, t, v + lane, tx, in, get);
         }
     }
 }
@@ -498,14 +531,15 @@ __global__ __launch_bounds__(kRowThreads) void sort_dispatch_kernel(
     // one vector a thread: the grid covers the row
     const int64_t v = (int64_t)blockIdx.y * kRowThreads + threadIdx.x;
     if (M::copy)
-        copy_vec(a.rows, t, v, true, a.k, get);  // past the row's end: counts, copies nothing
+        copy_vecs<1>(a.rows, t, v, 0, true, a.k, get);  // past the row's end: counts only
     else
-        quant_vec<M::pow2, M::narrow>(a, t, v, true, get);
+        quant_vecs<M>(a, t, v, 0, true, get);
 }
 
 // ---- weighted sum back, and the gradients -------------------------------------
 
-template <typename In, typename Out, bool kNarrow>
+// kCount slots of kVecs vectors at a time.
+template <typename In, typename Out, int kCount, int kVecs, bool kNarrow>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(
     const In *__restrict__ ys, int64_t ld, int64_t R, const int32_t *__restrict__ slot_row,
     const float *__restrict__ weights, RowShape shape, int64_t k, int64_t H,
@@ -516,44 +550,58 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(
     for (int64_t round = blockIdx.x; round < rounds; round += gridDim.x) {
         const int64_t own = round * per + (threadIdx.x >> shape.tx_log);
         const int64_t t = own < shape.T ? own : shape.T - 1;
-        for (int64_t v0 = (int64_t)blockIdx.y * tx; v0 < vecs; v0 += (int64_t)gridDim.y * tx) {
-            const int64_t v = v0 + lane;
-            const Span s = row_span(v, H);
-            float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            Raw8<Out> first;
-            zero_raw(first);
-            if (residual)
-                load_raw<kNarrow>(residual + t * ld_residual + s.col, s.hi, first);
-            if (k == 0) unpack(first, acc);
-            for (int64_t j0 = 0; j0 < k; j0 += kBatch) {
-                Batch<kBatch> batch;
-                Raw8<In> raw[kBatch];
+        for (int64_t v0 = (int64_t)blockIdx.y * tx * kVecs; v0 < vecs;
+             v0 += (int64_t)gridDim.y * tx * kVecs) {
+            Span s[kVecs];
+            float acc[kVecs][8] = {};
+            Raw8<Out> first[kVecs];
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                s[i] = row_span(v0 + lane + i * tx, H);
+                zero_raw(first[i]);
+                if (residual)
+                    load_raw<kNarrow>(residual + t * ld_residual + s[i].col, s[i].hi, first[i]);
+                if (k == 0) unpack(first[i], acc[i]);
+            }
+            for (int64_t j0 = 0; j0 < k; j0 += kCount) {
+                Batch<kCount> batch;
+                Raw8<In> raw[kVecs][kCount];
                 batch.load(slot_row, weights, t, k, j0);
                 batch.share(k, j0, R);
 #pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    zero_raw(raw[b]);
-                    if (batch.rows[b] >= 0)
-                        load_raw<kNarrow>(ys + (int64_t)batch.rows[b] * ld + s.col, s.hi, raw[b]);
-                }
-                if (j0 == 0) unpack(first, acc);
+                for (int b = 0; b < kCount; ++b)
 #pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    float f[8];
-                    unpack(raw[b], f);
+                    for (int i = 0; i < kVecs; ++i) {
+                        zero_raw(raw[i][b]);
+                        if (batch.rows[b] >= 0)
+                            load_raw<kNarrow>(ys + (int64_t)batch.rows[b] * ld + s[i].col, s[i].hi,
+                                              raw[i][b]);
+                    }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        acc[i] = batch.rows[b] < 0 ? acc[i]
-                                                   : __builtin_fmaf(batch.w[b], f[i], acc[i]);
+                for (int i = 0; i < kVecs; ++i) {
+                    if (j0 == 0) unpack(first[i], acc[i]);
+#pragma unroll
+                    for (int b = 0; b < kCount; ++b) {
+                        float f[8];
+                        unpack(raw[i][b], f);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            acc[i][c] = batch.rows[b] < 0
+                                            ? acc[i][c]
+                                            : __builtin_fmaf(batch.w[b], f[c], acc[i][c]);
+                    }
                 }
             }
-            if (own < shape.T && s.any()) store_span(out + t * H, s, acc);
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+                if (own < shape.T && s[i].any()) store_span(out + t * H, s[i], acc[i]);
         }
     }
 }
 
-// dys rows and the dot products: one token a workgroup, kCount slots at a time.
-template <typename V, int kThreads, int kCount, bool kNarrow>
+// dys rows and the dot products: one token a workgroup, kCount slots of kVecs
+// vectors at a time.
+template <typename V, int kThreads, int kCount, int kVecs, bool kNarrow>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(
     const V *__restrict__ dout, int64_t ld_dout, const V *__restrict__ ys, int64_t ld_ys,
     int64_t R, const int32_t *__restrict__ slot_row, const float *__restrict__ weights,
@@ -569,40 +617,48 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(
             batch.share(k, j0, R);
             const int32_t(&rows)[kCount] = batch.rows;
             const float(&w)[kCount] = batch.w;
-            for (int64_t v = threadIdx.x; v < vecs; v += blockDim.x) {
-                const Span s = row_span(v, H);
-                Raw8<V> raw, y[kCount];
-                load_raw<kNarrow>(dout + t * ld_dout + s.col, s.hi, raw);
-                if (dweights) {
+            for (int64_t v = threadIdx.x; v < vecs; v += kVecs * blockDim.x) {
+                Span s[kVecs];
+                Raw8<V> raw[kVecs], y[kVecs][kCount];
 #pragma unroll
-                    for (int b = 0; b < kCount; ++b) {
-                        zero_raw(y[b]);
-                        if (rows[b] >= 0)
-                            load_raw<kNarrow>(ys + (int64_t)rows[b] * ld_ys + s.col, s.hi, y[b]);
+                for (int i = 0; i < kVecs; ++i) {
+                    s[i] = row_span(v + i * (int)blockDim.x, H);
+                    load_raw<kNarrow>(dout + t * ld_dout + s[i].col, s[i].hi, raw[i]);
+                    if (dweights) {
+#pragma unroll
+                        for (int b = 0; b < kCount; ++b) {
+                            zero_raw(y[i][b]);
+                            if (rows[b] >= 0)
+                                load_raw<kNarrow>(ys + (int64_t)rows[b] * ld_ys + s[i].col,
+                                                  s[i].hi, y[i][b]);
+                        }
                     }
                 }
-                float d[8];
-                unpack_own(raw, s, d);
-                if (dys) {
 #pragma unroll
-                    for (int b = 0; b < kCount; ++b) {
-                        if (rows[b] < 0) continue;
-                        float g[8];
+                for (int i = 0; i < kVecs; ++i) {
+                    float d[8];
+                    unpack_own(raw[i], s[i], d);
+                    if (dys) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) g[i] = w[b] * d[i];
-                        store_span(dys + rows[b] * H, s, g);
+                        for (int b = 0; b < kCount; ++b) {
+                            if (rows[b] < 0 || !s[i].any()) continue;
+                            float g[8];
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) g[c] = w[b] * d[c];
+                            store_span(dys + rows[b] * H, s[i], g);
+                        }
                     }
-                }
-                if (dweights) {
+                    if (dweights) {
 #pragma unroll
-                    for (int b = 0; b < kCount; ++b) {
-                        float f[8];
-                        unpack_own(y[b], s, f);
-                        float sum = 0;
+                        for (int b = 0; b < kCount; ++b) {
+                            float f[8];
+                            unpack_own(y[i][b], s[i], f);
+                            float sum = 0;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(d[i], f[i], sum);
-                        // (a dropped slot has no product, not one with zero)
-                        dot[b] = rows[b] < 0 ? 0.0f : dot[b] + sum;
+                            for (int c = 0; c < 8; ++c) sum = __builtin_fmaf(d[c], f[c], sum);
+                            // (a dropped slot has no product, not one with zero)
+                            dot[b] = rows[b] < 0 ? 0.0f : dot[b] + sum;
+                        }
                     }
                 }
             }
@@ -661,10 +717,10 @@ GatherArgs quant_args(const void *x, int64_t ldx, int64_t H, int64_t k, void *q,
 
 // go(Gather<...>{}) for quantizing rows of H values.
 template <typename F>
-auto with_quant(bool pow2, int64_t H, F go) {
-    if (H >= 8)
-        return pow2 ? go(Gather<kQuantPow2, false>{}) : go(Gather<kQuant, false>{});
-    return pow2 ? go(Gather<kQuantPow2, true>{}) : go(Gather<kQuant, true>{});
+auto with_quant(bool pow2, int64_t H, bool many, F go) {
+    if (H < 8) return pow2 ? go(Gather<kQuantPow2, true, 1>{}) : go(Gather<kQuant, true, 1>{});
+    if (many) return pow2 ? go(Gather<kQuantPow2, false, 4>{}) : go(Gather<kQuant, false, 4>{});
+    return pow2 ? go(Gather<kQuantPow2, false, 1>{}) : go(Gather<kQuant, false, 1>{});
 }
 
 // Few slots: sort and gather in one launch, a workgroup for each token and
@@ -692,18 +748,23 @@ bool sort_dispatch_few(const MoeRouting &r, const GatherArgs &a, int64_t vecs,
 hipError_t launch_moe_dispatch(const GatherPlane &rows, const GatherPlane *scales,
                                const int32_t *slot_row, int64_t T, int64_t k, int64_t R,
                                hipStream_t stream) {
-    const RowGrid g = row_grid(T, (rows.bytes + 15) / 16, 16);
-    dispatch_kernel<Gather<kCopy, false>><<<g.grid, kRowThreads, 0, stream>>>(copy_args(rows, scales, k, R),
-                                                               g.shape, slot_row);
+    const int64_t vecs = (rows.bytes + 15) / 16;
+    const bool many = T * vecs >= kManyVecs;
+    const RowGrid g = row_grid(T, vecs, 16, many ? 4 : 1);
+    auto *kernel = many ? dispatch_kernel<Gather<kCopy, false, 4>>
+                        : dispatch_kernel<Gather<kCopy, false, 1>>;
+    kernel<<<g.grid, kRowThreads, 0, stream>>>(copy_args(rows, scales, k, R), g.shape, slot_row);
     return hipGetLastError();
 }
 
 hipError_t launch_moe_dispatch_quant(const void *x, int64_t ldx, int64_t T, int64_t H,
                                      const int32_t *slot_row, int64_t k, void *q, float *scales,
                                      int64_t R, bool pow2, hipStream_t stream) {
-    const RowGrid g = row_grid(T, (H + kGroup - 1) / kGroup * 16, 16);
-    with_quant(pow2, H, [&](auto m) {
-        dispatch_kernel<decltype(m)><<<g.grid, kRowThreads, 0, stream>>>(
+    const int64_t vecs = (H + kGroup - 1) / kGroup * 16;
+    with_quant(pow2, H, T * vecs >= kManyVecs, [&](auto m) {
+        using M = decltype(m);
+        const RowGrid g = row_grid(T, vecs, 16, M::vecs);
+        dispatch_kernel<M><<<g.grid, kRowThreads, 0, stream>>>(
             quant_args(x, ldx, H, k, q, scales, R), g.shape, slot_row);
     });
     return hipGetLastError();
@@ -712,7 +773,7 @@ hipError_t launch_moe_dispatch_quant(const void *x, int64_t ldx, int64_t T, int6
 hipError_t launch_moe_sort_dispatch(const MoeRouting &r, const GatherPlane &rows,
                                     hipStream_t stream) {
     const int64_t R = r.T * r.k;
-    if (sort_dispatch_few<Gather<kCopy, false>>(r, copy_args(rows, nullptr, r.k, R), (rows.bytes + 15) / 16,
+    if (sort_dispatch_few<Gather<kCopy, false, 1>>(r, copy_args(rows, nullptr, r.k, R), (rows.bytes + 15) / 16,
                                  stream))
         return hipGetLastError();
     const hipError_t e = launch_moe_sort(r, stream);
@@ -725,7 +786,7 @@ hipError_t launch_moe_sort_dispatch_quant(const MoeRouting &r, const void *x, in
                                           hipStream_t stream) {
     const int64_t R = r.T * r.k, vecs = (H + kGroup - 1) / kGroup * 16;
     const GatherArgs a = quant_args(x, ldx, H, r.k, q, scales, R);
-    if (with_quant(pow2, H,
+    if (with_quant(pow2, H, false,
                    [&](auto m) { return sort_dispatch_few<decltype(m)>(r, a, vecs, stream); }))
         return hipGetLastError();
     const hipError_t e = launch_moe_sort(r, stream);
@@ -738,11 +799,15 @@ hipError_t launch_moe_combine(const void *ys, bool ys_bf16, int64_t ld, int64_t 
                               const int32_t *slot_row, const float *weights, int64_t T,
                               int64_t k, int64_t H, const void *residual, int64_t ld_residual,
                               void *out, bool out_bf16, hipStream_t stream) {
-    const RowGrid g = row_grid(T, (H + 7) / 8, 16);
+    const int64_t vecs = (H + 7) / 8;
+    const bool few = k <= 2 && T * vecs >= kManyVecs;
+    const RowGrid g = row_grid(T, vecs, 16, few ? 4 : 1);
     auto go = [&](auto in, auto to) {
         using In = decltype(in);
         using Out = decltype(to);
-        auto *kernel = H >= 8 ? combine_kernel<In, Out, false> : combine_kernel<In, Out, true>;
+        auto *kernel = H < 8 ? combine_kernel<In, Out, kBatch, 1, true>
+                       : few ? combine_kernel<In, Out, 2, 4, false>
+                             : combine_kernel<In, Out, kBatch, 1, false>;
         kernel<<<g.grid, kRowThreads, 0, stream>>>(
             static_cast<const In *>(ys), ld, R, slot_row, weights, g.shape, k, H,
             static_cast<const Out *>(residual), ld_residual, static_cast<Out *>(out));
@@ -760,14 +825,17 @@ hipError_t launch_moe_combine_grad(const void *dout, int64_t ld_dout, const void
                                    const float *weights, int64_t T, int64_t k, int64_t H,
                                    void *dys, float *dweights, hipStream_t stream) {
     const unsigned blocks = (unsigned)(T < kMaxBlocks ? T : kMaxBlocks);
-    // Few tokens do not fill the card, so there a row has up to 1024 threads.
+    // Few tokens do not fill the card: there a row has up to 512 threads
+    // (one token of 7168 values to 8 experts: 10.5 us with 1024 threads and
+    // four slots at a time).
     const bool few = T < 256;
-    const int threads = threads_per_row((H + 7) / 8, 64, few ? 1024 : 256);
+    const int threads = threads_per_row((H + 7) / 8, 64, few ? 512 : 256);
     auto go = [&](auto v) {
         using V = decltype(v);
-        auto *kernel = H < 8  ? combine_grad_kernel<V, 256, 4, true>
-                       : few  ? combine_grad_kernel<V, 1024, 4, false>
-                              : combine_grad_kernel<V, 256, kBatch, false>;
+        auto *kernel = H < 8    ? combine_grad_kernel<V, 256, 4, 1, true>
+                       : few    ? combine_grad_kernel<V, 512, kBatch, 1, false>
+                       : k <= 2 ? combine_grad_kernel<V, 256, 2, 4, false>
+                                : combine_grad_kernel<V, 256, kBatch, 1, false>;
         kernel<<<blocks, threads, 0, stream>>>(static_cast<const V *>(dout), ld_dout,
                                                static_cast<const V *>(ys), ld_ys, R, slot_row,
                                                weights, T, k, H, static_cast<V *>(dys), dweights);

@@ -85,7 +85,8 @@ def _fn(name):
 
 
 def _call(name, *args):
-    status = _fn(name)(*args)
+    f = _functions.get(name) or _fn(name)
+    status = f(*args)
     if status:
         raise Fp8Error(status, name)
 
@@ -135,17 +136,24 @@ def _rows(t, name, dtypes, shape=None):
 def _disjoint(t, name, others):
     """Refuse an output whose memory is an input's: the kernels read inputs
     after they have begun to write outputs."""
-    if t is None or t.numel() == 0:
+    if t is None:
         return
     a0 = t.data_ptr()
-    a1 = a0 + t.numel() * t.element_size()
+    a1 = a0 + t.nbytes
     for other, what in others:
-        if other is None or other.numel() == 0:
+        # what begins behind the output (or holds nothing) cannot share it
+        if other is None or other.data_ptr() >= a1:
             continue
-        b0 = other.data_ptr()
+        if other.numel() == 0:
+            continue
         span = sum((n - 1) * s for n, s in zip(other.shape, other.stride())) + 1
-        if b0 < a1 and a0 < b0 + span * other.element_size():
+        if a0 < other.data_ptr() + span * other.element_size():
             raise ValueError(f"{name} must not share memory with {what}")
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
+_empty = torch.empty
 
 
 class _Place:
@@ -153,40 +161,47 @@ class _Place:
     device and the stream current while outputs are allocated and the work is
     enqueued, and gives the stream's handle."""
 
-    __slots__ = ("device", "stream", "handle", "tensors", "outer")
+    __slots__ = ("device", "stream", "handle", "tensors", "outer", "scratch")
 
-    def __init__(self, stream, **tensors):
-        self.device = None
-        self.stream = stream
-        self.tensors = tensors
-        for name, t in tensors.items():
+    def __init__(self, stream, names, *tensors):
+        device = None
+        for t in tensors:
             if t is None:
                 continue
             if not t.is_cuda:
-                raise ValueError(f"{name} must be on the GPU")
-            if self.device is None:
-                self.device = t.device
-            elif t.device != self.device:
-                raise ValueError(f"{name} must be on {self.device}, got {t.device}")
-        if stream is not None and stream.device != self.device:
-            raise ValueError(f"stream must be on {self.device}, got {stream.device}")
+                raise ValueError(f"{self._name(names, tensors, t)} must be on the GPU")
+            if device is None:
+                device = t.device
+            elif t.device != device:
+                raise ValueError(f"{self._name(names, tensors, t)} must be on {device}, got "
+                                 f"{t.device}")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream must be on {device}, got {stream.device}")
+        self.device = device
+        self.stream = stream
+        self.tensors = tensors
+
+    @staticmethod
+    def _name(names, tensors, t):
+        return next(n for n, u in zip(names.split(), tensors) if u is t)
 
     def __enter__(self):
         self.outer = None
+        index = self.device.index
         if self.stream is not None:
             self.outer = torch.cuda.stream(self.stream)
             self.outer.__enter__()
-            for t in self.tensors.values():
+            for t in self.tensors:
                 if t is not None:
                     t.record_stream(self.stream)
-        elif self.device.index != torch.cuda.current_device():
+        elif index != _current_device():
             self.outer = torch.cuda.device(self.device)
             self.outer.__enter__()
-        self.handle = torch.cuda.current_stream(self.device).cuda_stream
+        self.handle = _raw_stream(index)
         return self
 
     def empty(self, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=self.device)
+        return _empty(shape, dtype=dtype, device=self.device)
 
     def workspace(self, given, nbytes):
         """(pointer, bytes) of the workspace, allocated if it is needed and
@@ -194,8 +209,7 @@ class _Place:
         if given is None:
             if nbytes == 0:
                 return None, 0
-            given = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-            self.tensors["workspace"] = given
+            given = self.scratch = _empty(nbytes, dtype=torch.uint8, device=self.device)
         return given.data_ptr(), given.numel() * given.element_size()
 
     def __exit__(self, *exc):
@@ -266,8 +280,8 @@ def fp8_moe_sort(expert_ids, num_experts, group_offsets=None, slot_row=None, row
     (-1 for a dropped slot), row_slot int32 [T k] (-1 past the kept rows))."""
     _check_ids(expert_ids, num_experts, group_offsets, slot_row, row_slot, workspace)
     T, k = expert_ids.shape
-    with _Place(stream, expert_ids=expert_ids, group_offsets=group_offsets, slot_row=slot_row,
-                row_slot=row_slot, workspace=workspace) as p:
+    with _Place(stream, "expert_ids group_offsets slot_row row_slot workspace",
+                expert_ids, group_offsets, slot_row, row_slot, workspace) as p:
         plan = _plan(p, expert_ids, num_experts, group_offsets, slot_row, row_slot)
         ws, ws_bytes = p.workspace(workspace, fp8_moe_sort_workspace_bytes(T, k, num_experts))
         _call("fp8_moe_sort", expert_ids.data_ptr(), expert_ids.element_size(), T, k, num_experts,
@@ -319,7 +333,8 @@ def fp8_moe_dispatch(x, slot_row, scales=None, xs=None, xs_scales=None, stream=N
     elif xs_scales is not None:
         raise ValueError("xs_scales given without scales")
     _disjoint(xs, "xs", ((x, "x"), (slot_row, "slot_row")))
-    with _Place(stream, x=x, slot_row=slot_row, scales=scales, xs=xs, xs_scales=xs_scales) as p:
+    with _Place(stream, "x slot_row scales xs xs_scales",
+                x, slot_row, scales, xs, xs_scales) as p:
         if xs is None:
             xs = p.empty((rows, H), x.dtype)
         if scales is not None and xs_scales is None:
@@ -341,7 +356,8 @@ def _dispatch_quant(name, x, slot_row, q, scales, stream):
     rows = q.shape[0] if q is not None else scales.shape[0] if scales is not None else T * k
     if scales is not None:
         _dense(scales, "scales", (rows, G), _F32)
-    with _Place(stream, x=x, slot_row=slot_row, q=q, scales=scales) as p:
+    with _Place(stream, "x slot_row q scales",
+                x, slot_row, q, scales) as p:
         if q is None:
             q = p.empty((rows, H), torch.uint8)
         if scales is None:
@@ -374,8 +390,8 @@ def fp8_moe_sort_dispatch(x, expert_ids, num_experts, group_offsets=None, slot_r
     if xs is not None:
         _dense(xs, "xs", (T * k, H), (x.dtype,))
         _disjoint(xs, "xs", ((x, "x"), (expert_ids, "expert_ids")))
-    with _Place(stream, x=x, expert_ids=expert_ids, group_offsets=group_offsets,
-                slot_row=slot_row, row_slot=row_slot, xs=xs, workspace=workspace) as p:
+    with _Place(stream, "x expert_ids group_offsets slot_row row_slot xs workspace",
+                x, expert_ids, group_offsets, slot_row, row_slot, xs, workspace) as p:
         plan = _plan(p, expert_ids, num_experts, group_offsets, slot_row, row_slot)
         if xs is None:
             xs = p.empty((T * k, H), x.dtype)
@@ -399,9 +415,8 @@ def _sort_dispatch_quant(name, x, expert_ids, num_experts, group_offsets, slot_r
         _dense(q, "q", (T * k, H), _U8)
     if scales is not None:
         _dense(scales, "scales", (T * k, G), _F32)
-    with _Place(stream, x=x, expert_ids=expert_ids, group_offsets=group_offsets,
-                slot_row=slot_row, row_slot=row_slot, q=q, scales=scales,
-                workspace=workspace) as p:
+    with _Place(stream, "x expert_ids group_offsets slot_row row_slot q scales workspace",
+                x, expert_ids, group_offsets, slot_row, row_slot, q, scales, workspace) as p:
         plan = _plan(p, expert_ids, num_experts, group_offsets, slot_row, row_slot)
         if q is None:
             q = p.empty((T * k, H), torch.uint8)
@@ -446,7 +461,8 @@ def fp8_moe_dispatch_grad(dxs, slot_row, dx=None, out_dtype=None, stream=None):
     if dx is not None:
         _dense(dx, "dx", (T, H), tuple(d for d in _WIDE if d == dtype) or _WIDE)
         _disjoint(dx, "dx", ((dxs, "dxs"), (slot_row, "slot_row")))
-    with _Place(stream, dxs=dxs, slot_row=slot_row, dx=dx) as p:
+    with _Place(stream, "dxs slot_row dx",
+                dxs, slot_row, dx) as p:
         if dx is None:
             dx = p.empty((T, H), dtype)
         _call("fp8_moe_dispatch_grad", dxs.data_ptr(), _CODES[dxs.dtype], ld, R,
@@ -478,8 +494,8 @@ def fp8_moe_combine(ys, slot_row, weights=None, residual=None, out=None, out_dty
         if residual is not None and not (residual.data_ptr() == out.data_ptr()
                                          and ld_residual == H):
             _disjoint(out, "out", ((residual, "residual (unless it is residual)"),))
-    with _Place(stream, ys=ys, slot_row=slot_row, weights=weights, residual=residual,
-                out=out) as p:
+    with _Place(stream, "ys slot_row weights residual out",
+                ys, slot_row, weights, residual, out) as p:
         if out is None:
             out = p.empty((T, H), dtype)
         _call("fp8_moe_combine", ys.data_ptr(), _CODES[ys.dtype], ld, R, slot_row.data_ptr(),
@@ -509,8 +525,8 @@ def fp8_moe_combine_grad(dout, ys, slot_row, weights=None, dys=None, dweights=No
                                (weights, "weights")))
     if dweights is not None:
         _dense(dweights, "dweights", (T, k), _F32)
-    with _Place(stream, dout=dout, ys=ys, slot_row=slot_row, weights=weights, dys=dys,
-                dweights=dweights) as p:
+    with _Place(stream, "dout ys slot_row weights dys dweights",
+                dout, ys, slot_row, weights, dys, dweights) as p:
         if dys is None:
             dys = p.empty((R, H), dout.dtype)
         if dweights is None:
@@ -572,8 +588,8 @@ def _norm(name, quant, y, r, w_post, gate, w_pre, post_norm, residual_scale, bra
     for what, t in (("rstd_post", rstd_post), ("rstd_pre", rstd_pre)):
         if t is not None:
             _dense(t, what, (T,), _F32)
-    with _Place(stream, y=y, r=r, w_post=w_post, gate=gate, w_pre=w_pre, r_out=r_out, n=n, q=q,
-                scales=scales, rstd_post=rstd_post, rstd_pre=rstd_pre) as p:
+    with _Place(stream, "y r w_post gate w_pre r_out n q scales rstd_post rstd_pre",
+                y, r, w_post, gate, w_pre, r_out, n, q, scales, rstd_post, rstd_pre) as p:
         if r_out is None:
             r_out = p.empty((T, H), r.dtype)
         if quant:
@@ -671,9 +687,9 @@ def fp8_norm_residual_grad(dn, dr_out, y, r_out, rstd_post, rstd_pre, w_post=Non
         _dense(dr, "dr", (T, H), (r_out.dtype,))
         _disjoint(dr, "dr", read + ((dy, "dy"),))
     _workspace_tensor(workspace)
-    with _Place(stream, dn=dn, dr_out=dr_out, y=y, r_out=r_out, rstd_post=rstd_post,
-                rstd_pre=rstd_pre, w_post=w_post, gate=gate, w_pre=w_pre, dy=dy, dr=dr,
-                workspace=workspace) as p:
+    with _Place(stream, "dn dr_out y r_out rstd_post rstd_pre w_post gate w_pre dy dr workspace",
+                dn, dr_out, y, r_out, rstd_post, rstd_pre, w_post, gate, w_pre, dy, dr,
+                workspace) as p:
         if dy is None:
             dy = p.empty((T, H), y.dtype)
         if dr is None:
@@ -707,7 +723,8 @@ def _w4_quant(name, w, group, scale_type, codes, scales, stream):
         _dense(codes, "codes", code_shape, _U8)
     if scales is not None:
         _dense(scales, "scales", scale_shape, (scale_type,))
-    with _Place(stream, w=w, codes=codes, scales=scales) as p:
+    with _Place(stream, "w codes scales",
+                w, codes, scales) as p:
         if codes is None:
             codes = p.empty(code_shape, torch.uint8)
         if scales is None:
@@ -756,7 +773,8 @@ def fp8_w4_matvec(x, codes, scales, out_dtype="bf16", y=None, stream=None):
     if y is not None:
         _dense(y, "y", (M, N), (dtype,))
         _disjoint(y, "y", ((x, "x"), (codes, "codes"), (scales, "scales")))
-    with _Place(stream, x=x, codes=codes, scales=scales, y=y) as p:
+    with _Place(stream, "x codes scales y",
+                x, codes, scales, y) as p:
         if y is None:
             y = p.empty((M, N), dtype)
         _call("fp8_w4_matvec", x.data_ptr(), ldx, codes.data_ptr(), scales.data_ptr(), kind, M, N,
@@ -778,7 +796,8 @@ def fp8_w4_grouped_matvec(x, codes, scales, group_offsets, out_dtype="bf16", y=N
         _dense(y, "y", (R, N), (dtype,))
         _disjoint(y, "y", ((x, "x"), (codes, "codes"), (scales, "scales"),
                            (group_offsets, "group_offsets")))
-    with _Place(stream, x=x, codes=codes, scales=scales, group_offsets=group_offsets, y=y) as p:
+    with _Place(stream, "x codes scales group_offsets y",
+                x, codes, scales, group_offsets, y) as p:
         if y is None:
             y = p.empty((R, N), dtype)
         _call("fp8_w4_grouped_matvec", x.data_ptr(), ldx, codes.data_ptr(), scales.data_ptr(),
