@@ -114,12 +114,10 @@ __global__ __launch_bounds__(B::threads) void norm_kernel(NormArgs a, int tx, in
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) span[j] = row_span(lane + (int64_t)j * tx, a.H);
     load_row(t0);
-    float w_post[kVecs][8], w_pre[kVecs][8], gate[kVecs][8];
+    float q[kVecs][8], w_pre[kVecs][8];  // q = branch_scale gate w_post
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-        load_param<B::narrow>(a.post ? a.w_post : nullptr, a.param_bf16, 0, span[j], w_post[j]);
+    for (int j = 0; j < kVecs; ++j)
         load_param<B::narrow>(want_n ? a.w_pre : nullptr, a.param_bf16, 0, span[j], w_pre[j]);
-    }
     int64_t gate_row = t0 / per_gate - 1, gate_end = (gate_row + 1) * per_gate;
     for (int64_t t = t0; t < t1; ++t) {
         float y[kVecs][8], s[kVecs][8];
@@ -134,8 +132,13 @@ __global__ __launch_bounds__(B::threads) void norm_kernel(NormArgs a, int tx, in
             ++gate_row;
             gate_end = (gate_row + 1) * per_gate;
 #pragma unroll
-            for (int j = 0; j < kVecs; ++j)
-                load_param<B::narrow>(a.gate, a.param_bf16, gate_row * a.H, span[j], gate[j]);
+            for (int j = 0; j < kVecs; ++j) {
+                float w[8];
+                load_param<B::narrow>(a.gate, a.param_bf16, gate_row * a.H, span[j], q[j]);
+                load_param<B::narrow>(a.post ? a.w_post : nullptr, a.param_bf16, 0, span[j], w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q[j][i] = a.branch_scale * q[j][i] * w[i];
+            }
         }
         float rs1 = 1.0f;
         if (a.post) {
@@ -152,8 +155,7 @@ __global__ __launch_bounds__(B::threads) void norm_kernel(NormArgs a, int tx, in
         for (int j = 0; j < kVecs; ++j) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float u = a.post ? y[j][i] * rs1 * w_post[j][i] : y[j][i];
-                s[j][i] = a.residual_scale * s[j][i] + a.branch_scale * gate[j][i] * u;
+                s[j][i] = a.residual_scale * s[j][i] + q[j][i] * (y[j][i] * rs1);
                 sum[0] = __builtin_fmaf(s[j][i], s[j][i], sum[0]);
             }
             store_span(static_cast<S *>(a.r_out) + t * a.H, span[j], s[j]);

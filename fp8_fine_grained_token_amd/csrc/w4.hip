@@ -106,7 +106,6 @@ __global__ __launch_bounds__(256) void w4_quant_kernel(const uint16_t *__restric
 // same stretches, and of the 16 x 16 products only those of equal stretches
 // are added up.  That makes tiles of 8 or 4 columns, for outputs too narrow
 // to fill the card with tiles of 16.
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
