@@ -22,6 +22,7 @@ inline void clear_last_error() { (void)hipGetLastError(); }
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 constexpr int64_t kMaxInner = (int64_t)1 << 24;  // inner dimension of a 4-bit product
+constexpr int64_t kMaxWidth = (int64_t)1 << 28;  // a token's row: 32-bit byte offsets
 
 inline bool dim_ok(int64_t n) { return n >= 0 && n < kMaxDim; }
 inline bool matrix_ok(int64_t rows, int64_t cols) {
@@ -54,7 +55,7 @@ fp8_status check_routing(const MoeRouting &r, int id_bytes, size_t workspace_byt
 
 // A plan and the rows it names: T x k slots into R rows.
 fp8_status check_plan(const int32_t *slot_row, int64_t T, int64_t k, int64_t H, int64_t R) {
-    if (!matrix_ok(T, H) || !matrix_ok(R, H)) return FP8_ERR_SHAPE;
+    if (!matrix_ok(T, H) || !matrix_ok(R, H) || H >= kMaxWidth) return FP8_ERR_SHAPE;
     if (!dim_ok(k) || T * k >= kMaxDim) return FP8_ERR_SHAPE;
     if (T * k > 0 && H > 0) {
         if (!slot_row) return FP8_ERR_NULL;

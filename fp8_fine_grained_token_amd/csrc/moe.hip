@@ -372,16 +372,14 @@ __device__ __forceinline__ void quant_vecs(const GatherArgs &a, int64_t t, int64
     float scale[M::vecs];
 #pragma unroll
     for (int i = 0; i < M::vecs; ++i) {
-        s[i] = row_span(v + i * step, a.H);
+        s[i] = row_span<M::narrow>(v + i * step, a.H);
         load_raw<M::narrow>(a.x + t * a.ldx + s[i].col, s[i].hi, raw[i]);
     }
 #pragma unroll
     for (int i = 0; i < M::vecs; ++i) {
         float f[8];
         unpack_own(raw[i], s[i], f);
-        const QuotientCtx qc(row16_max(absmax8(f)), M::pow2);
-        bytes[i] = quant8(f, qc);
-        scale[i] = qc.s;
+        bytes[i] = quantize8(f, row16_max(absmax8(f)), s[i].any(), M::pow2, scale[i]);
     }
     for (int64_t j0 = 0; j0 < a.k; j0 += kBatch) {
         int32_t rows[kBatch];
@@ -557,7 +555,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(
             Raw8<Out> first[kVecs];
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                s[i] = row_span(v0 + lane + i * tx, H);
+                s[i] = row_span<kNarrow>(v0 + lane + i * tx, H);
                 zero_raw(first[i]);
                 if (residual)
                     load_raw<kNarrow>(residual + t * ld_residual + s[i].col, s[i].hi, first[i]);
@@ -622,7 +620,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(
                 Raw8<V> raw[kVecs], y[kVecs][kCount];
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
-                    s[i] = row_span(v + i * (int)blockDim.x, H);
+                    s[i] = row_span<kNarrow>(v + i * (int)blockDim.x, H);
                     load_raw<kNarrow>(dout + t * ld_dout + s[i].col, s[i].hi, raw[i]);
                     if (dweights) {
 #pragma unroll

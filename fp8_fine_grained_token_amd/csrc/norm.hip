@@ -41,11 +41,19 @@ __device__ __forceinline__ void row_sum(float (&v)[kSums], int tx, float *lds, i
 #pragma unroll
         for (int i = 0; i < kSums; ++i) part[(threadIdx.x >> 6) * kSums + i] = v[i];
     __syncthreads();
+    // up to 16 waves: lane w takes wave w's sums
+    const int w = threadIdx.x & 15;
 #pragma unroll
     for (int i = 0; i < kSums; ++i) {
-        v[i] = 0;
-        for (int w = 0; w < (int)blockDim.x / 64; ++w) v[i] += part[w * kSums + i];
+        v[i] = w < (int)blockDim.x / 64 ? part[w * kSums + i] : 0.0f;
+#pragma unroll
+        for (int m = 8; m; m /= 2) v[i] += __shfl_xor(v[i], m);
     }
+}
+
+template <typename T>
+__device__ __forceinline__ const T *in_row(const void *p, int64_t row_at, const Span &s) {
+    return span_at(static_cast<const T *>(p) + row_at, s);
 }
 
 // A parameter's values of a span (ones without one).
@@ -57,25 +65,67 @@ __device__ __forceinline__ void load_param(const void *p, bool bf16, int64_t at,
         for (int i = 0; i < 8; ++i) f[i] = 1.0f;
     } else if (bf16) {
         Raw8<Bf16> r;
-        load_raw<kNarrow>(static_cast<const Bf16 *>(p) + at + s.col, s.hi, r);
+        load_raw<kNarrow>(in_row<Bf16>(p, at, s), s.hi, r);
         unpack(r, f);
     } else {
         Raw8<float> r;
-        load_raw<kNarrow>(static_cast<const float *>(p) + at + s.col, s.hi, r);
+        load_raw<kNarrow>(in_row<float>(p, at, s), s.hi, r);
         unpack(r, f);
     }
 }
 
 // How a kernel is built: y's and the stream's type, vectors of a row that a
-// thread holds (lane, lane + tx, ...), rows of up to 64 threads (kSmall: many
-// to a workgroup, sums inside a wave) and rows of fewer than eight values.
-template <typename Y_, typename S_, int kVecs_, bool kSmall_, bool kNarrow_>
+// thread holds (lane, lane + tx, ...), the most threads of a workgroup, rows of
+// up to 64 threads (kSmall: many to a workgroup, sums inside a wave) and rows
+// of fewer than eight values.
+template <typename Y_, typename S_, int kVecs_, int kThreads_, bool kSmall_, bool kNarrow_>
 struct Build {
     using Y = Y_;
     using S = S_;
-    static constexpr int vecs = kVecs_;
+    static constexpr int vecs = kVecs_, threads = kThreads_;
     static constexpr bool small = kSmall_, narrow = kNarrow_;
-    static constexpr int threads = kSmall_ ? kSmallThreads : 1024;
+    // Waves a SIMD should hold in the forward kernel: two workgroups of up to
+    // 16 waves need eight (rows of 7168 values, 14 waves: with seven a second
+    // workgroup did not fit, 57 us against 52 for 4096 rows).
+    static constexpr int waves = kSmall_ || kVecs_ > 1 ? 4 : kThreads_ > 512 ? 8 : 6;
+};
+
+// Rows wider than this are not held in registers (beyond two vectors a thread
+// the forward spills, beyond one the gradient).
+constexpr int64_t kHeldForward = 16384, kHeldGrad = 8192;
+
+// A parameter of a thread's columns, kept over its rows: in registers for
+// short rows, in LDS (each thread its own 32 bytes a vector, no barrier) for
+// the others, where two workgroups then fit a compute unit or the gradient
+// stays clear of spills.
+template <int kVecs, int kThreads, bool kSmall>
+struct Kept {
+    float f[kVecs][8];
+    static constexpr int floats = 4;
+    __device__ __forceinline__ explicit Kept(float4 *) {}
+    __device__ __forceinline__ void put(int j, const float (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[j][i] = v[i];
+    }
+    __device__ __forceinline__ void get(int j, float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = f[j][i];
+    }
+};
+template <int kVecs, int kThreads>
+struct Kept<kVecs, kThreads, false> {
+    float4 *mine;
+    static constexpr int floats = 8 * kThreads * kVecs;
+    __device__ __forceinline__ explicit Kept(float4 *lds) : mine(lds + threadIdx.x) {}
+    __device__ __forceinline__ void put(int j, const float (&v)[8]) {
+        mine[2 * kThreads * j] = make_float4(v[0], v[1], v[2], v[3]);
+        mine[2 * kThreads * j + kThreads] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    __device__ __forceinline__ void get(int j, float (&v)[8]) const {
+        const float4 a = mine[2 * kThreads * j], b = mine[2 * kThreads * j + kThreads];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
 };
 
 // Which row's threads these are: `member` counts workgroups, or rows' threads.
@@ -85,11 +135,14 @@ __device__ __forceinline__ int64_t member_of(int tx) {
 }
 
 template <typename B, bool kQuant>
-__global__ __launch_bounds__(B::threads) void norm_kernel(NormArgs a, int tx, int64_t rows_each) {
+__global__ __launch_bounds__(B::threads, B::waves) void norm_kernel(NormArgs a, int tx,
+                                                                    int64_t rows_each) {
     using Y = typename B::Y;
     using S = typename B::S;
     constexpr int kVecs = B::vecs;
+    using Param = Kept<kVecs, B::threads, B::small>;
     __shared__ float lds[2 * 16];
+    __shared__ float4 kept[2][Param::floats / 4];
     int turn = 0;
     const int lane = B::small ? threadIdx.x & (tx - 1) : threadIdx.x;
     const int64_t t0 = member_of<B::small>(tx) * rows_each;
@@ -105,19 +158,20 @@ __global__ __launch_bounds__(B::threads) void norm_kernel(NormArgs a, int tx, in
     auto load_row = [&](int64_t t) {
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            load_raw<B::narrow>(static_cast<const Y *>(a.y) + t * a.ldy + span[j].col, span[j].hi,
-                                y_raw[j]);
-            load_raw<B::narrow>(static_cast<const S *>(a.r) + t * a.ldr + span[j].col, span[j].hi,
-                                r_raw[j]);
+            load_raw<B::narrow>(in_row<Y>(a.y, t * a.ldy, span[j]), span[j].hi, y_raw[j]);
+            load_raw<B::narrow>(in_row<S>(a.r, t * a.ldr, span[j]), span[j].hi, r_raw[j]);
         }
     };
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) span[j] = row_span(lane + (int64_t)j * tx, a.H);
+    for (int j = 0; j < kVecs; ++j) span[j] = row_span<B::narrow>(lane + j * tx, a.H);
     load_row(t0);
-    float q[kVecs][8], w_pre[kVecs][8];  // q = branch_scale gate w_post
+    Param q(kept[0]), w_pre(kept[1]);  // q = branch_scale gate w_post
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j)
-        load_param<B::narrow>(want_n ? a.w_pre : nullptr, a.param_bf16, 0, span[j], w_pre[j]);
+    for (int j = 0; j < kVecs; ++j) {
+        float w[8];
+        load_param<B::narrow>(want_n ? a.w_pre : nullptr, a.param_bf16, 0, span[j], w);
+        w_pre.put(j, w);
+    }
     int64_t gate_row = t0 / per_gate - 1, gate_end = (gate_row + 1) * per_gate;
     for (int64_t t = t0; t < t1; ++t) {
         float y[kVecs][8], s[kVecs][8];
@@ -133,11 +187,12 @@ __global__ __launch_bounds__(B::threads) void norm_kernel(NormArgs a, int tx, in
             gate_end = (gate_row + 1) * per_gate;
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
-                float w[8];
-                load_param<B::narrow>(a.gate, a.param_bf16, gate_row * a.H, span[j], q[j]);
+                float w[8], g[8];
+                load_param<B::narrow>(a.gate, a.param_bf16, gate_row * a.H, span[j], g);
                 load_param<B::narrow>(a.post ? a.w_post : nullptr, a.param_bf16, 0, span[j], w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) q[j][i] = a.branch_scale * q[j][i] * w[i];
+                for (int i = 0; i < 8; ++i) g[i] = a.branch_scale * g[i] * w[i];
+                q.put(j, g);
             }
         }
         float rs1 = 1.0f;
@@ -153,9 +208,11 @@ __global__ __launch_bounds__(B::threads) void norm_kernel(NormArgs a, int tx, in
         sum[0] = 0;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
+            float w[8];
+            q.get(j, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                s[j][i] = a.residual_scale * s[j][i] + q[j][i] * (y[j][i] * rs1);
+                s[j][i] = a.residual_scale * s[j][i] + w[i] * (y[j][i] * rs1);
                 sum[0] = __builtin_fmaf(s[j][i], s[j][i], sum[0]);
             }
             store_span(static_cast<S *>(a.r_out) + t * a.H, span[j], s[j]);
@@ -166,16 +223,99 @@ __global__ __launch_bounds__(B::threads) void norm_kernel(NormArgs a, int tx, in
         if (a.rstd_pre && lane == 0) a.rstd_pre[t] = rs2;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
+            float w[8];
+            w_pre.get(j, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[j][i] = s[j][i] * rs2 * w_pre[j][i];
+            for (int i = 0; i < 8; ++i) s[j][i] = s[j][i] * rs2 * w[i];
             if (a.n) store_span(static_cast<Y *>(a.n) + t * a.H, span[j], s[j]);
             if (kQuant) {
-                const QuotientCtx qc(row16_max(absmax8(s[j])), a.pow2);
-                store_e4m3(static_cast<uint8_t *>(a.q) + t * a.H, span[j], quant8(s[j], qc));
+                float scale;
+                const uint2 bytes = quantize8(s[j], row16_max(absmax8(s[j])), span[j].any(),
+                                              a.pow2, scale);
+                store_e4m3(static_cast<uint8_t *>(a.q) + t * a.H, span[j], bytes);
                 if ((lane & 15) == 0 && span[j].any())
-                    a.scales[t * G + (lane + (int64_t)j * tx) / 16] = qc.s;
+                    a.scales[t * G + (lane + (int64_t)j * tx) / 16] = scale;
             }
         }
+    }
+}
+
+// Wide rows, one a workgroup: read once for y's sum, once for the new
+// stream's, and once more (from L2) for the results.
+template <typename Y, typename S, bool kQuant>
+__global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs a) {
+    __shared__ float lds[2 * 16];
+    int turn = 0;
+    const float inv_h = 1.0f / (float)a.H;
+    const int64_t per_gate = a.T / a.gate_rows, G = (a.H + kGroup - 1) / kGroup;
+    const int vecs = (int)((a.H + 7) / 8), step = blockDim.x;
+    const void *post_weights = a.post ? a.w_post : nullptr;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const int64_t gate_at = t / per_gate * a.H;
+        float sum[1] = {0};
+        // every thread takes every turn: the sums and 16-lane maxima need all
+        auto row = [&](auto use) {
+            for (int v0 = 0; v0 < vecs; v0 += step) {
+                const Span span = row_span<false>(v0 + (int)threadIdx.x, a.H);
+                Raw8<Y> y_raw;
+                load_raw<false>(in_row<Y>(a.y, t * a.ldy, span), span.hi, y_raw);
+                float y[8];
+                unpack_own(y_raw, span, y);
+                use(v0 + (int)threadIdx.x, span, y);
+            }
+        };
+        float rs1 = 1.0f;
+        if (a.post) {
+            row([&](int, const Span &, const float(&y)[8]) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(y[i], y[i], sum[0]);
+            });
+            row_sum<1, false>(sum, 0, lds, turn);
+            rs1 = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
+            if (a.rstd_post && threadIdx.x == 0) a.rstd_post[t] = rs1;
+        }
+        auto stream = [&](const Span &span, const float(&y)[8], float(&s)[8]) {
+            Raw8<S> raw;
+            load_raw<false>(in_row<S>(a.r, t * a.ldr, span), span.hi, raw);
+            float w[8], g[8];
+            load_param<false>(post_weights, a.param_bf16, 0, span, w);
+            load_param<false>(a.gate, a.param_bf16, gate_at, span, g);
+            unpack_own(raw, span, s);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                s[i] = a.residual_scale * s[i] + a.branch_scale * g[i] * w[i] * (y[i] * rs1);
+        };
+        const bool want_n = a.n || kQuant;
+        float rs2 = 1.0f;
+        if (want_n) {
+            sum[0] = 0;
+            row([&](int, const Span &span, const float(&y)[8]) {
+                float s[8];
+                stream(span, y, s);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(s[i], s[i], sum[0]);
+            });
+            row_sum<1, false>(sum, 0, lds, turn);
+            rs2 = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
+            if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[t] = rs2;
+        }
+        row([&](int v, const Span &span, const float(&y)[8]) {
+            float s[8], w[8];
+            stream(span, y, s);
+            store_span(static_cast<S *>(a.r_out) + t * a.H, span, s);
+            if (!want_n) return;
+            load_param<false>(a.w_pre, a.param_bf16, 0, span, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] = s[i] * rs2 * w[i];
+            if (a.n) store_span(static_cast<Y *>(a.n) + t * a.H, span, s);
+            if (kQuant) {
+                float scale;
+                const uint2 bytes =
+                    quantize8(s, row16_max(absmax8(s)), span.any(), a.pow2, scale);
+                store_e4m3(static_cast<uint8_t *>(a.q) + t * a.H, span, bytes);
+                if ((threadIdx.x & 15) == 0 && span.any()) a.scales[t * G + v / 16] = scale;
+            }
+        });
     }
 }
 
@@ -189,6 +329,9 @@ __global__ __launch_bounds__(B::threads) void norm_kernel(NormArgs a, int tx, in
 // Both means of a row come from one round of sums: with e = dr', q = b g w1,
 //   c1 = sum A rh / H,  D = e + rs2 (A - rh c1),
 //   c2 = sum q D yh / H = (sum q yh (e + rs2 A) - rs2 c1 sum q yh rh) / H.
+// For wide rows a kernel of its own finds rs2 c1 and c2 of every row first
+// (kGiven); the rest needs nothing of other columns, so a workgroup then takes
+// a stretch of columns.
 // Within a gate row, dg = b w1 sum D yh and its part of dw1 = b g sum D yh, so
 // one running sum (of D yh) serves both until the gate row ends.
 struct GradPlan {
@@ -214,17 +357,21 @@ GradPlan grad_plan(int64_t T, int64_t gate_rows, int64_t most) {
     return p;
 }
 
-template <typename B>
+template <typename B, bool kGiven>
 __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradPlan p, int tx,
+                                                               const float2 *given,
                                                                float *part_post, float *part_pre,
                                                                float *part_gate) {
     using Y = typename B::Y;
     using S = typename B::S;
     constexpr int kVecs = B::vecs;
+    using Param = Kept<kVecs, B::threads, B::small>;
     __shared__ float lds[2 * 16 * 3];
+    __shared__ float4 kept[2][Param::floats / 4];
     int turn = 0;
     const int lane = B::small ? threadIdx.x & (tx - 1) : threadIdx.x;
     const int64_t member = member_of<B::small>(tx);
+    const int first_vec = kGiven ? blockIdx.y * tx : 0;
     if (member >= p.members) return;  // all threads of the row
     int64_t t0, t1;
     if (p.chunks == 1) {
@@ -241,28 +388,26 @@ __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradP
     Raw8<Y> y_raw[kVecs], dn_raw[kVecs];
     float rs1_next = 1.0f, rs2_next = 0.0f;  // (read with the row: behind the stores they would wait for them)
     Raw8<S> r_raw[kVecs], e_raw[kVecs];
+    float2 c_next = {0, 0};
     auto load_row = [&](int64_t t) {
+        if (kGiven) c_next = given[t];
         if (a.dn) rs2_next = a.in_rstd_pre[t];
         if (a.post) rs1_next = a.in_rstd_post[t];
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            load_raw<B::narrow>(static_cast<const Y *>(a.y) + t * a.ldy + span[j].col, span[j].hi,
-                                y_raw[j]);
+            load_raw<B::narrow>(in_row<Y>(a.y, t * a.ldy, span[j]), span[j].hi, y_raw[j]);
             if (a.dn) {
-                load_raw<B::narrow>(static_cast<const Y *>(a.dn) + t * a.ld_dn + span[j].col,
-                                    span[j].hi, dn_raw[j]);
-                load_raw<B::narrow>(static_cast<const S *>(a.r) + t * a.ldr + span[j].col,
-                                    span[j].hi, r_raw[j]);
+                load_raw<B::narrow>(in_row<Y>(a.dn, t * a.ld_dn, span[j]), span[j].hi, dn_raw[j]);
+                load_raw<B::narrow>(in_row<S>(a.r, t * a.ldr, span[j]), span[j].hi, r_raw[j]);
             }
             if (a.dr_out)
-                load_raw<B::narrow>(
-                    static_cast<const S *>(a.dr_out) + t * a.ld_dr_out + span[j].col, span[j].hi,
-                    e_raw[j]);
+                load_raw<B::narrow>(in_row<S>(a.dr_out, t * a.ld_dr_out, span[j]), span[j].hi,
+                                    e_raw[j]);
         }
     };
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-        span[j] = row_span(lane + (int64_t)j * tx, a.H);
+        span[j] = row_span<B::narrow>(first_vec + lane + j * tx, a.H);
         zero_raw(dn_raw[j]);
         zero_raw(r_raw[j]);
         zero_raw(e_raw[j]);
@@ -270,12 +415,15 @@ __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradP
     if (t0 < t1) load_row(t0);
     // q = b g w1, w2; sums of D yh (this gate row) and of dw2's terms; the
     // member's part of dw1 grows in its partial row, once a gate row
-    float q[kVecs][8], w2[kVecs][8];
+    Param q(kept[0]), w2(kept[1]);
     float acc[kVecs][8] = {}, acc2[kVecs][8] = {};
     const void *post_weights = a.post ? a.w_post : nullptr;
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j)
-        load_param<B::narrow>(a.dn ? a.w_pre : nullptr, a.param_bf16, 0, span[j], w2[j]);
+    for (int j = 0; j < kVecs; ++j) {
+        float w[8];
+        load_param<B::narrow>(a.dn ? a.w_pre : nullptr, a.param_bf16, 0, span[j], w);
+        w2.put(j, w);
+    }
     int64_t gate_row = 0, gate_end = 0;
     bool first_gate = true;
     auto begin_gate_row = [&](int64_t row) {
@@ -283,11 +431,12 @@ __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradP
         gate_end = (row + 1) * p.per_gate;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            float w1[8];
+            float w1[8], g[8];
             load_param<B::narrow>(post_weights, a.param_bf16, 0, span[j], w1);
-            load_param<B::narrow>(a.gate, a.param_bf16, gate_row * a.H, span[j], q[j]);
+            load_param<B::narrow>(a.gate, a.param_bf16, gate_row * a.H, span[j], g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q[j][i] = a.branch_scale * q[j][i] * w1[i];
+            for (int i = 0; i < 8; ++i) g[i] = a.branch_scale * g[i] * w1[i];
+            q.put(j, g);
         }
     };
     auto end_gate_row = [&] {
@@ -323,6 +472,7 @@ __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradP
     if (t0 < t1) begin_gate_row(t0 / p.per_gate);
     for (int64_t t = t0; t < t1; ++t) {
         const float rs1 = rs1_next, rs2 = rs2_next;
+        float c1 = c_next.x, c2 = c_next.y;
         float A[kVecs][8], rh[kVecs][8], yh[kVecs][8], e[kVecs][8];
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
@@ -338,31 +488,38 @@ __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradP
         }
         float sum[3] = {0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j)
+        for (int j = 0; j < kVecs; ++j) {
+            float w[8], qv[8];
+            w2.get(j, w);
+            q.get(j, qv);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 yh[j][i] *= rs1;
                 rh[j][i] *= rs2;
                 acc2[j][i] = __builtin_fmaf(A[j][i], rh[j][i], acc2[j][i]);
-                A[j][i] *= w2[j][i];
+                A[j][i] *= w[i];
                 sum[0] = __builtin_fmaf(A[j][i], rh[j][i], sum[0]);
                 e[j][i] = __builtin_fmaf(rs2, A[j][i], e[j][i]);
-                const float qy = q[j][i] * yh[j][i];
+                const float qy = qv[i] * yh[j][i];
                 sum[1] = __builtin_fmaf(qy, e[j][i], sum[1]);
                 sum[2] = __builtin_fmaf(qy, rh[j][i], sum[2]);
             }
-        row_sum<3, B::small>(sum, tx, lds, turn);
-        const float c1 = rs2 * sum[0] * inv_h;
-        const float c2 = a.post ? (sum[1] - c1 * sum[2]) * inv_h : 0.0f;
+        }
+        if (!kGiven) {
+            row_sum<3, B::small>(sum, tx, lds, turn);
+            c1 = rs2 * sum[0] * inv_h;
+            c2 = a.post ? (sum[1] - c1 * sum[2]) * inv_h : 0.0f;
+        }
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            float dr[8], dy[8];
+            float dr[8], dy[8], qv[8];
+            q.get(j, qv);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float D = __builtin_fmaf(-c1, rh[j][i], e[j][i]);
                 dr[i] = a.residual_scale * D;
                 acc[j][i] = __builtin_fmaf(D, yh[j][i], acc[j][i]);
-                dy[i] = rs1 * (D * q[j][i] - yh[j][i] * c2);
+                dy[i] = rs1 * (D * qv[i] - yh[j][i] * c2);
             }
             store_span(static_cast<S *>(a.dr) + t * a.H, span[j], dr);
             store_span(static_cast<Y *>(a.dy) + t * a.H, span[j], dy);
@@ -372,6 +529,58 @@ __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradP
     if (a.dw_pre)
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) store_span(part_pre + member * a.H, span[j], acc2[j]);
+}
+
+// (rs2 c1, c2) of wide rows, one a workgroup.
+template <typename Y, typename S>
+__global__ __launch_bounds__(1024) void norm_grad_sums_kernel(NormArgs a, float2 *given) {
+    __shared__ float lds[2 * 16 * 3];
+    int turn = 0;
+    const float inv_h = 1.0f / (float)a.H;
+    const int64_t per_gate = a.T / a.gate_rows;
+    const int vecs = (int)((a.H + 7) / 8);
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const float rs2 = a.dn ? a.in_rstd_pre[t] : 0.0f;
+        const float rs1 = a.post ? a.in_rstd_post[t] : 1.0f;
+        float sum[3] = {0, 0, 0};
+        for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
+            const Span span = row_span<false>(v, a.H);
+            Raw8<Y> y_raw, dn_raw;
+            Raw8<S> r_raw, e_raw;
+            zero_raw(dn_raw);
+            zero_raw(r_raw);
+            zero_raw(e_raw);
+            load_raw<false>(in_row<Y>(a.y, t * a.ldy, span), span.hi, y_raw);
+            if (a.dn) {
+                load_raw<false>(in_row<Y>(a.dn, t * a.ld_dn, span), span.hi, dn_raw);
+                load_raw<false>(in_row<S>(a.r, t * a.ldr, span), span.hi, r_raw);
+            }
+            if (a.dr_out)
+                load_raw<false>(in_row<S>(a.dr_out, t * a.ld_dr_out, span), span.hi, e_raw);
+            float w1[8], w2[8], g[8], y[8], A[8], rh[8], e[8];
+            load_param<false>(a.post ? a.w_post : nullptr, a.param_bf16, 0, span, w1);
+            load_param<false>(a.dn ? a.w_pre : nullptr, a.param_bf16, 0, span, w2);
+            load_param<false>(a.gate, a.param_bf16, t / per_gate * a.H, span, g);
+            unpack_own(y_raw, span, y);
+            unpack_own(dn_raw, span, A);
+            unpack_own(r_raw, span, rh);
+            unpack_own(e_raw, span, e);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                A[i] *= w2[i];
+                rh[i] *= rs2;
+                sum[0] = __builtin_fmaf(A[i], rh[i], sum[0]);
+                e[i] = __builtin_fmaf(rs2, A[i], e[i]);
+                const float qy = a.branch_scale * g[i] * w1[i] * (y[i] * rs1);
+                sum[1] = __builtin_fmaf(qy, e[i], sum[1]);
+                sum[2] = __builtin_fmaf(qy, rh[i], sum[2]);
+            }
+        }
+        row_sum<3, false>(sum, 0, lds, turn);
+        const float c1 = rs2 * sum[0] * inv_h;
+        if (threadIdx.x == 0)
+            given[t] = make_float2(c1, a.post ? (sum[1] - c1 * sum[2]) * inv_h : 0.0f);
+    }
 }
 
 // out[group][h] = sum over the group's `rows` partial rows: 64 columns a
@@ -427,33 +636,24 @@ RowSplit row_split(int64_t H) {
         return s;
     }
     s.small = false;
-    s.vecs = 1;
-    while (s.vecs * 1024 < vecs) s.vecs *= 2;
+    s.vecs = vecs <= 1024 ? 1 : 2;
     s.tx = s.block = (int)((((vecs + s.vecs - 1) / s.vecs) + 63) / 64 * 64);
     return s;
 }
 
-// f(Build<...>{}) for the types and the split at hand.
-template <typename Y, typename S, typename F>
-void with_split(const RowSplit &s, int64_t H, F f) {
-    if (H < 8) f(Build<Y, S, 1, true, true>{});
-    else if (s.small) f(Build<Y, S, 1, true, false>{});
-    else if (s.vecs == 1) f(Build<Y, S, 1, false, false>{});
-    else if (s.vecs == 2) f(Build<Y, S, 2, false, false>{});
-    else f(Build<Y, S, 4, false, false>{});
-}
-
+// f(Y{}, S{}) for the types at hand.
 template <typename F>
-void with_build(const NormArgs &a, const RowSplit &s, F f) {
-    if (a.y_bf16 && a.r_bf16) with_split<Bf16, Bf16>(s, a.H, f);
-    else if (a.y_bf16) with_split<Bf16, float>(s, a.H, f);
-    else with_split<float, float>(s, a.H, f);
+void with_types(const NormArgs &a, F f) {
+    if (a.y_bf16 && a.r_bf16) f(Bf16{}, Bf16{});
+    else if (a.y_bf16) f(Bf16{}, float{});
+    else f(float{}, float{});
 }
 
 // Members that share the rows: enough workgroups to fill the card, as few
 // partial rows as that allows.
-int64_t grad_members(const RowSplit &s) {
-    return s.small ? 512 * (kSmallThreads / s.tx) : s.block >= 512 ? 512 : 1024;
+int64_t grad_members(int64_t H) {
+    const RowSplit s = row_split(H);
+    return s.small ? 512 * (kSmallThreads / s.tx) : H > 1024 ? 512 : 1024;
 }
 
 }  // namespace
@@ -462,38 +662,78 @@ hipError_t launch_norm_residual(const NormArgs &a, hipStream_t stream) {
     const RowSplit s = row_split(a.H);
     const int64_t per = s.small ? kSmallThreads / s.tx : 1;
     int64_t blocks = (a.T + per - 1) / per;
-    const int64_t most = s.block >= 512 ? 512 : 2048;
+    const int64_t most = s.small || s.block < 512 ? 2048 : 512;
     int64_t rows_each = 1;
     if (blocks > most) {
         rows_each = (a.T + most * per - 1) / (most * per);
         blocks = (a.T + rows_each * per - 1) / (rows_each * per);
     }
-    with_build(a, s, [&](auto b) {
-        using B = decltype(b);
-        auto *kernel = a.q ? norm_kernel<B, true> : norm_kernel<B, false>;
-        kernel<<<(unsigned)blocks, s.block, 0, stream>>>(a, s.tx, rows_each);
+    with_types(a, [&](auto y, auto r) {
+        using Y = decltype(y);
+        using S = decltype(r);
+        if (a.H > kHeldForward) {
+            auto *kernel = a.q ? norm_wide_kernel<Y, S, true> : norm_wide_kernel<Y, S, false>;
+            kernel<<<(unsigned)(a.T < 2048 ? a.T : 2048), 1024, 0, stream>>>(a);
+            return;
+        }
+        auto go = [&](auto b) {
+            using B = decltype(b);
+            auto *kernel = a.q ? norm_kernel<B, true> : norm_kernel<B, false>;
+            kernel<<<(unsigned)blocks, s.block, 0, stream>>>(a, s.tx, rows_each);
+        };
+        if (a.H < 8) go(Build<Y, S, 1, kSmallThreads, true, true>{});
+        else if (s.small) go(Build<Y, S, 1, kSmallThreads, true, false>{});
+        else if (s.vecs == 2) go(Build<Y, S, 2, 1024, false, false>{});
+        else if (s.block <= 256) go(Build<Y, S, 1, 256, false, false>{});
+        else if (s.block <= 512) go(Build<Y, S, 1, 512, false, false>{});
+        else go(Build<Y, S, 1, 1024, false, false>{});
     });
     return hipGetLastError();
 }
 
 size_t norm_grad_workspace_bytes(int64_t T, int64_t H, int64_t gate_rows) {
     if (T == 0 || H == 0) return 0;
-    const GradPlan p = grad_plan(T, gate_rows, grad_members(row_split(H)));
-    return (size_t)(p.chunks > 1 ? 3 : 2) * p.members * H * sizeof(float);
+    const GradPlan p = grad_plan(T, gate_rows, grad_members(H));
+    return ((size_t)(p.chunks > 1 ? 3 : 2) * p.members * H + (H > kHeldGrad ? 2 * T : 0)) *
+           sizeof(float);
 }
 
 hipError_t launch_norm_residual_grad(const NormArgs &a, hipStream_t stream) {
     const RowSplit s = row_split(a.H);
+    const bool wide = a.H > kHeldGrad;
     GradPlan p = {1, 1, 1, 0};
-    if (a.T > 0) p = grad_plan(a.T, a.gate_rows, grad_members(s));
-    float *part_post = a.workspace, *part_pre = part_post + p.members * a.H;
-    float *part_gate = part_pre + p.members * a.H;
+    if (a.T > 0) p = grad_plan(a.T, a.gate_rows, grad_members(a.H));
+    // wide rows' coefficients first: two floats a row, 16-byte aligned
+    float2 *given = reinterpret_cast<float2 *>(a.workspace);
+    float *part_post = a.workspace + (wide ? 2 * a.T : 0);
+    float *part_pre = part_post + p.members * a.H, *part_gate = part_pre + p.members * a.H;
     if (a.T > 0) {
         const int64_t per = s.small ? kSmallThreads / s.tx : 1;
-        const int64_t blocks = (p.members + per - 1) / per;
-        with_build(a, s, [&](auto b) {
-            norm_grad_kernel<decltype(b)><<<(unsigned)blocks, s.block, 0, stream>>>(
-                a, p, s.tx, part_post, part_pre, part_gate);
+        const unsigned blocks = (unsigned)((p.members + per - 1) / per);
+        with_types(a, [&](auto y, auto r) {
+            using Y = decltype(y);
+            using S = decltype(r);
+            auto go = [&](auto b) {
+                norm_grad_kernel<decltype(b), false><<<blocks, s.block, 0, stream>>>(
+                    a, p, s.tx, nullptr, part_post, part_pre, part_gate);
+            };
+            if (wide) {
+                const unsigned rows = (unsigned)(a.T < 2048 ? a.T : 2048);
+                norm_grad_sums_kernel<Y, S><<<rows, 1024, 0, stream>>>(a, given);
+                const dim3 grid(blocks, (unsigned)((a.H + 8 * 256 - 1) / (8 * 256)));
+                norm_grad_kernel<Build<Y, S, 1, 256, false, false>, true>
+                    <<<grid, 256, 0, stream>>>(a, p, 256, given, part_post, part_pre, part_gate);
+            } else if (a.H < 8) {
+                go(Build<Y, S, 1, kSmallThreads, true, true>{});
+            } else if (s.small) {
+                go(Build<Y, S, 1, kSmallThreads, true, false>{});
+            } else if (s.block <= 256) {
+                go(Build<Y, S, 1, 256, false, false>{});
+            } else if (s.block <= 512) {
+                go(Build<Y, S, 1, 512, false, false>{});
+            } else {
+                go(Build<Y, S, 1, 1024, false, false>{});
+            }
         });
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;

@@ -11,6 +11,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_common.hpp"
 
 namespace fp8blk {
@@ -44,17 +46,18 @@ __device__ __forceinline__ void from_float(float f, Bf16 &v) { v.bits = (uint16_
 // index lo up to hi are its own (none past the last vector; hi < 8 only in
 // rows of fewer than eight values).
 struct Span {
-    int64_t col;
-    int lo, hi;
+    int col, lo, hi;
     __device__ __forceinline__ bool whole() const { return lo == 0 && hi == 8; }
     __device__ __forceinline__ bool any() const { return lo < hi; }
     __device__ __forceinline__ bool has(int i) const { return i >= lo && i < hi; }
 };
 
+template <bool kNarrow>
 __device__ __forceinline__ Span row_span(int64_t v, int64_t H) {
     Span s;
-    s.hi = H < 8 ? (int)H : 8;
-    s.col = 8 * v < H - s.hi ? 8 * v : H - s.hi;
+    s.hi = kNarrow ? (int)H : 8;
+    const int64_t most = H - s.hi;
+    s.col = (int)(8 * v < most ? 8 * v : most);
     const int64_t over = 8 * v - s.col;
     s.lo = over < 8 ? (int)over : 8;
     return s;
@@ -120,6 +123,15 @@ __device__ __forceinline__ void unpack_own(const Raw8<T> &r, const Span &s, floa
     }
 }
 
+// Where a span begins in a row, by a 32-bit byte offset (rows are below 2^30
+// bytes): next to a row address that a wave shares it is all a lane keeps.
+template <typename T>
+__device__ __forceinline__ T *span_at(T *row, const Span &s) {
+    using Byte = typename std::conditional<std::is_const<T>::value, const char, char>::type;
+    return reinterpret_cast<T *>(reinterpret_cast<Byte *>(row) +
+                                 (uint32_t)s.col * (uint32_t)sizeof(T));
+}
+
 // The span's own values to a row.
 __device__ __forceinline__ void store_span(Bf16 *row, const Span &s, const float (&f)[8]) {
     if (s.whole()) {
@@ -128,11 +140,11 @@ __device__ __forceinline__ void store_span(Bf16 *row, const Span &s, const float
         v.y = to_bf16x2(f[2], f[3]);
         v.z = to_bf16x2(f[4], f[5]);
         v.w = to_bf16x2(f[6], f[7]);
-        *reinterpret_cast<u32x4_any *>(row + s.col) = v;
+        *reinterpret_cast<u32x4_any *>(span_at(row, s)) = v;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (s.has(i)) from_float(f[i], row[s.col + i]);
+            if (s.has(i)) from_float(f[i], span_at(row, s)[i]);
     }
 }
 __device__ __forceinline__ void store_span(float *row, const Span &s, const float (&f)[8]) {
@@ -142,26 +154,47 @@ __device__ __forceinline__ void store_span(float *row, const Span &s, const floa
         a.z = __float_as_uint(f[2]); a.w = __float_as_uint(f[3]);
         b.x = __float_as_uint(f[4]); b.y = __float_as_uint(f[5]);
         b.z = __float_as_uint(f[6]); b.w = __float_as_uint(f[7]);
-        *reinterpret_cast<u32x4_any *>(row + s.col) = a;
-        *reinterpret_cast<u32x4_any *>(row + s.col + 4) = b;
+        *reinterpret_cast<u32x4_any *>(span_at(row, s)) = a;
+        *reinterpret_cast<u32x4_any *>(span_at(row, s) + 4) = b;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (s.has(i)) row[s.col + i] = f[i];
+            if (s.has(i)) span_at(row, s)[i] = f[i];
     }
 }
+// E4M3 bytes and scale of a lane's part of a 1x128 group of maximum `amax`
+// (`used`: the lane holds any of it).  The usual groups take a path without
+// branches and with one divide (the activation quantizer's); a wave with an
+// all-zero or tiny group takes the general one.
+__device__ __forceinline__ uint2 quantize8(const float (&f)[8], float amax, bool used, bool pow2,
+                                           float &scale) {
+    if (__all(!used || (pow2 ? amax > 0.0f : amax >= 0x1p-60f))) {
+        scale = pow2 ? scale_pow2(amax) : scale_fast(amax);
+        const float r = 1.0f / scale;
+        uint32_t lo = 0, hi = 0;
+        lo = cvt_pk_e4m3<false>(quot_fast(f[0], scale, r), quot_fast(f[1], scale, r), lo);
+        lo = cvt_pk_e4m3<true>(quot_fast(f[2], scale, r), quot_fast(f[3], scale, r), lo);
+        hi = cvt_pk_e4m3<false>(quot_fast(f[4], scale, r), quot_fast(f[5], scale, r), hi);
+        hi = cvt_pk_e4m3<true>(quot_fast(f[6], scale, r), quot_fast(f[7], scale, r), hi);
+        return make_uint2(lo, hi);
+    }
+    const QuotientCtx qc(amax, pow2);
+    scale = qc.s;
+    return quant8(f, qc);
+}
+
 // E4M3 bytes of the span's values of a 1x128 group.
 __device__ __forceinline__ void store_e4m3(uint8_t *row, const Span &s, uint2 v) {
     if (s.whole()) {
         u32x2_any w;
         w.x = v.x;
         w.y = v.y;
-        *reinterpret_cast<u32x2_any *>(row + s.col) = w;
+        *reinterpret_cast<u32x2_any *>(span_at(row, s)) = w;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (s.has(i))
-                row[s.col + i] = (uint8_t)((i < 4 ? v.x >> (8 * i) : v.y >> (8 * (i - 4))) & 0xFF);
+                span_at(row, s)[i] = (uint8_t)((i < 4 ? v.x >> (8 * i) : v.y >> (8 * (i - 4))) & 0xFF);
     }
 }
 

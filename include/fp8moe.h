@@ -32,6 +32,7 @@ extern "C" {
 #endif
 
 /* ---- tokens sorted by expert and back ---------------------------------- */
+/* H < 2^28 in all of them. */
 
 /*
  * Stable counting sort of the slots (t, j) of a routing by expert: what the
@@ -130,7 +131,8 @@ fp8_status fp8_moe_combine(const void *ys, int in_dtype, int64_t ld_ys, int64_t 
  *   dys[slot_row[t][j]] = weights[t][j] dout[t]
  *   dweights[t][j]      = sum_h dout[t][h] ys[slot_row[t][j]][h]  (0 if dropped)
  *   dout [T][H], ys [R][H] and dys [R][H] of dtype; dweights [T][top_k] fp32
- * dys or dweights may be NULL (not computed); ys may be NULL with dweights.
+ * dys or dweights may be NULL (not computed); without dweights ys is not read
+ * and may be NULL.
  * weights NULL means ones.  Rows of dys that no slot names are left
  * untouched.  (The residual's gradient is dout itself.)
  */
