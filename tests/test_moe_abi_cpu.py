@@ -6,6 +6,7 @@ or is a documented no-op)."""
 import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 import torch
@@ -37,6 +38,17 @@ def test_every_declared_symbol_is_exported_and_bound():
     import fp8_fine_grained_token_amd as F
     for name in declared():
         assert getattr(F, name) is getattr(M, name)
+
+
+def test_header_is_plain_c():
+    # a C99 program that includes the header and names every function
+    names = sorted(declared())
+    program = "#include \"fp8moe.h\"\n" + "".join(
+        f"void *p{i} = (void *)&{n};\n" for i, n in enumerate(names))
+    r = subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-fsyntax-only", "-x", "c",
+                        "-I" + os.path.join(ROOT, "include"), "-"], input=program, text=True,
+                       capture_output=True)
+    assert r.returncode == 0, r.stderr
 
 
 def sort(ids=A, b=8, T=4, k=2, E=8, off=A, sr=A, rs=A, ws=N, wsb=0):
