@@ -236,14 +236,15 @@ hipError_t sort_typed(const MoeRouting &r, hipStream_t stream) {
 // to a workgroup, the workgroups of gridDim.y side by side along wide rows.
 // A token's slots are read kBatch at a time, the row numbers of a batch in
 // one go and then the rows, so that a wait covers a batch and not a slot.
-// Where that leaves a thread with one or two loads (the gather reads a row
-// once; few slots a token), it takes four vectors at a time, unless there are
-// too few rows to give every thread work (kManyVecs).
+// Where that leaves a thread with few loads (the gather reads a row once; four
+// slots a token or fewer), it takes two or four vectors at a time, unless there
+// are too few rows to give every thread work (kManyVecs).
 constexpr int kRowThreads = 256;
 constexpr int kBatch = 8;
 constexpr int64_t kMaxBlocks = (int64_t)1 << 22;
-// Vectors over which a thread takes four: 8192 rows of 7168 values once each,
-// quantized gather 63 -> 44 us, weighted sum 99 -> 50 us.
+// Vectors from which a thread takes several: 8192 rows of 7168 values once
+// each, quantized gather 63 -> 44 us, weighted sum 99 -> 50 us; weighted sum of
+// four rows of 2048 values for 2048 tokens 10.0 -> 8.9 us.
 constexpr int64_t kManyVecs = (int64_t)1 << 19;
 
 struct RowShape {
@@ -542,7 +543,7 @@ __global__ __launch_bounds__(kRowThreads) void sort_dispatch_kernel(
 // ---- weighted sum back, and the gradients -------------------------------------
 
 // kCount slots of kVecs vectors at a time.
-template <typename In, typename Out, int kCount, int kVecs, bool kNarrow>
+template <typename In, typename Out, int kCount, int kVecs, bool kNarrow, bool kOnce>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(
     const In *__restrict__ ys, int64_t ld, int64_t R, const int32_t *__restrict__ slot_row,
     const float *__restrict__ weights, RowShape shape, int64_t k, int64_t H,
@@ -577,8 +578,8 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(
                     for (int i = 0; i < kVecs; ++i) {
                         zero_raw(raw[i][b]);
                         if (batch.rows[b] >= 0)
-                            load_raw<kNarrow>(ys + (int64_t)batch.rows[b] * ld + s[i].col, s[i].hi,
-                                              raw[i][b]);
+                            load_raw<kNarrow, kOnce>(ys + (int64_t)batch.rows[b] * ld + s[i].col,
+                                                     s[i].hi, raw[i][b]);
                     }
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
@@ -604,7 +605,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(
 
 // dys rows and the dot products: one token a workgroup, kCount slots of kVecs
 // vectors at a time.
-template <typename V, int kThreads, int kCount, int kVecs, bool kNarrow>
+template <typename V, int kThreads, int kCount, int kVecs, bool kNarrow, bool kOnce>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(
     const V *__restrict__ dout, int64_t ld_dout, const V *__restrict__ ys, int64_t ld_ys,
     int64_t R, const int32_t *__restrict__ slot_row, const float *__restrict__ weights,
@@ -632,7 +633,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(
                         for (int b = 0; b < kCount; ++b) {
                             zero_raw(y[i][b]);
                             if (rows[b] >= 0)
-                                load_raw<kNarrow>(ys + (int64_t)rows[b] * ld_ys + s[i].col,
+                                load_raw<kNarrow, kOnce>(ys + (int64_t)rows[b] * ld_ys + s[i].col,
                                                   s[i].hi, y[i][b]);
                         }
                     }
@@ -798,19 +799,35 @@ hipError_t launch_moe_sort_dispatch_quant(const MoeRouting &r, const void *x, in
                                                        R, pow2, stream);
 }
 
+namespace {
+
+// Whether the kept rows are loaded as read once, without a place in the
+// caches: from 96 MiB on, more than the caches keep until the next reader
+// (weighted sum of 8 rows of 7168 bf16 values for 4096 tokens, rows just
+// written: 227 us with the write, against 260; cold 97 against 109; gradient
+// for 2048 tokens 85 against 103; at 59 MB the other way, 13.8 against 12.3).
+bool read_once(int64_t rows, int64_t row_bytes) { return rows * row_bytes >= 96 << 20; }
+
+}  // namespace
+
 hipError_t launch_moe_combine(const void *ys, bool ys_bf16, int64_t ld, int64_t R,
                               const int32_t *slot_row, const float *weights, int64_t T,
                               int64_t k, int64_t H, const void *residual, int64_t ld_residual,
                               void *out, bool out_bf16, hipStream_t stream) {
     const int64_t vecs = (H + 7) / 8;
-    const bool few = k <= 2 && T * vecs >= kManyVecs;
-    const RowGrid g = row_grid(T, vecs, 16, few ? 4 : 1);
+    const bool once = read_once(T * k, H * (ys_bf16 ? 2 : 4));
+    const int per = k > 4 || T * vecs < kManyVecs ? 1 : k > 2 ? 2 : 4;
+    const RowGrid g = row_grid(T, vecs, 16, per);
     auto go = [&](auto in, auto to) {
         using In = decltype(in);
         using Out = decltype(to);
-        auto *kernel = H < 8 ? combine_kernel<In, Out, kBatch, 1, true>
-                       : few ? combine_kernel<In, Out, 2, 4, false>
-                             : combine_kernel<In, Out, kBatch, 1, false>;
+        auto *kernel = H < 8  ? combine_kernel<In, Out, kBatch, 1, true, false>
+                       : once ? per == 4   ? combine_kernel<In, Out, 2, 4, false, true>
+                                : per == 2 ? combine_kernel<In, Out, 4, 2, false, true>
+                                           : combine_kernel<In, Out, kBatch, 1, false, true>
+                       : per == 4 ? combine_kernel<In, Out, 2, 4, false, false>
+                       : per == 2 ? combine_kernel<In, Out, 4, 2, false, false>
+                                  : combine_kernel<In, Out, kBatch, 1, false, false>;
         kernel<<<g.grid, kRowThreads, 0, stream>>>(
             static_cast<const In *>(ys), ld, R, slot_row, weights, g.shape, k, H,
             static_cast<const Out *>(residual), ld_residual, static_cast<Out *>(out));
@@ -828,17 +845,26 @@ hipError_t launch_moe_combine_grad(const void *dout, int64_t ld_dout, const void
                                    const float *weights, int64_t T, int64_t k, int64_t H,
                                    void *dys, float *dweights, hipStream_t stream) {
     const unsigned blocks = (unsigned)(T < kMaxBlocks ? T : kMaxBlocks);
+    const int64_t vecs = (H + 7) / 8;
+    const bool once = read_once(T * k, H * (bf16 ? 2 : 4));
     // Few tokens do not fill the card: there a row has up to 512 threads
     // (one token of 7168 values to 8 experts: 10.5 us with 1024 threads and
-    // four slots at a time).
+    // four slots at a time).  Else a thread that would have four slots or
+    // fewer to load takes two or four vectors, and the row the fewer threads
+    // (4096 tokens of 2048 values: 4 slots 48 -> 29 us, 2 slots 22 -> 16).
     const bool few = T < 256;
-    const int threads = threads_per_row((H + 7) / 8, 64, few ? 512 : 256);
+    const int per = few ? 1 : k <= 2 ? 4 : k <= 4 ? 2 : 1;
+    const int threads = threads_per_row((vecs + per - 1) / per, 64, few ? 512 : 256);
     auto go = [&](auto v) {
         using V = decltype(v);
-        auto *kernel = H < 8    ? combine_grad_kernel<V, 256, 4, 1, true>
-                       : few    ? combine_grad_kernel<V, 512, kBatch, 1, false>
-                       : k <= 2 ? combine_grad_kernel<V, 256, 2, 4, false>
-                                : combine_grad_kernel<V, 256, kBatch, 1, false>;
+        auto *kernel = H < 8  ? combine_grad_kernel<V, 256, 4, 1, true, false>
+                       : few  ? combine_grad_kernel<V, 512, kBatch, 1, false, false>
+                       : once ? per == 4   ? combine_grad_kernel<V, 256, 2, 4, false, true>
+                                : per == 2 ? combine_grad_kernel<V, 256, 4, 2, false, true>
+                                           : combine_grad_kernel<V, 256, kBatch, 1, false, true>
+                       : per == 4 ? combine_grad_kernel<V, 256, 2, 4, false, false>
+                       : per == 2 ? combine_grad_kernel<V, 256, 4, 2, false, false>
+                                  : combine_grad_kernel<V, 256, kBatch, 1, false, false>;
         kernel<<<blocks, threads, 0, stream>>>(static_cast<const V *>(dout), ld_dout,
                                                static_cast<const V *>(ys), ld_ys, R, slot_row,
                                                weights, T, k, H, static_cast<V *>(dys), dweights);

@@ -76,22 +76,28 @@ struct Raw8<float> {
 
 // The eight values from p on; in rows of fewer than eight (kNarrow) those
 // there are, the last one repeated.  A template parameter: as a branch it
-// would put a wait after every load.
-template <bool kNarrow>
+// would put a wait after every load.  kOnce: values that are read this once
+// and need no place in the caches.
+template <bool kOnce>
+__device__ __forceinline__ u32x4_any load16(const void *p) {
+    const u32x4_any *v = static_cast<const u32x4_any *>(p);
+    return kOnce ? __builtin_nontemporal_load(v) : *v;
+}
+template <bool kNarrow, bool kOnce = false>
 __device__ __forceinline__ void load_raw(const Bf16 *p, int hi, Raw8<Bf16> &r) {
     if (!kNarrow) {
-        r.v = *reinterpret_cast<const u32x4_any *>(p);
+        r.v = load16<kOnce>(p);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             r.v[i] = p[min(2 * i, hi - 1)].bits | (uint32_t)p[min(2 * i + 1, hi - 1)].bits << 16;
     }
 }
-template <bool kNarrow>
+template <bool kNarrow, bool kOnce = false>
 __device__ __forceinline__ void load_raw(const float *p, int hi, Raw8<float> &r) {
     if (!kNarrow) {
-        r.a = *reinterpret_cast<const u32x4_any *>(p);
-        r.b = *reinterpret_cast<const u32x4_any *>(p + 4);
+        r.a = load16<kOnce>(p);
+        r.b = load16<kOnce>(p + 4);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

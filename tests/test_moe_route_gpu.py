@@ -267,6 +267,36 @@ def test_combine_grad_against_formula(T, k, E, H, drop, dtype):
     assert np.array_equal(f64(one_dys)[kept], dn[tok])
 
 
+@pytest.mark.parametrize("dtype,T,k,H", [("bf16", 9000, 6, 1001), ("bf16", 18000, 3, 1000),
+                                         ("bf16", 30000, 2, 1001), ("f32", 2100, 5, 2500)])
+def test_many_rows(dtype, T, k, H):
+    # more than 96 MiB of rows, and few and many slots a token
+    t = torch()
+    E = 16
+    _, slot_row, _ = plan_of(routing(T, T, k, E, 0.1), E)
+    s = cuda(slot_row)
+    ys, w, dout = draw(1, (T * k, H), dtype), draw(2, (T, k), "f32"), draw(3, (T, H), dtype)
+    out = M.fp8_moe_combine(ys, s, w)
+    dys, dw = M.fp8_moe_combine_grad(dout, ys, s, w, dys=t.zeros_like(ys))
+    want_dys = t.zeros(T * k, H, dtype=t.float64, device="cuda")
+    sums = t.zeros(T, H, dtype=t.float64, device="cuda")
+    mags, dots, dot_mags = sums.clone(), w.double() * 0, w.double() * 0
+    for j in range(k):
+        kept = (s[:, j] >= 0).double()[:, None]
+        rows = s[:, j].clamp(min=0).long()
+        terms = ys[rows].double() * kept * w[:, j, None].double()
+        sums += terms
+        mags += terms.abs()
+        products = ys[rows].double() * kept * dout.double()
+        dots[:, j], dot_mags[:, j] = products.sum(1), products.abs().sum(1)
+        at = s[:, j] >= 0
+        want_dys[rows[at]] = w[at, j, None].double() * dout[at].double()
+    close(out, f64(sums), f64(mags), k + 1)
+    # a thread adds 8 ceil(H / 512) products at most, then a tree of threads
+    close(dw, f64(dots), f64(dot_mags), 8 * -(-H // 512) + 30)
+    close(dys, f64(want_dys), f64(want_dys.abs()), 1)
+
+
 def test_gradients_against_differences():
     # the maps are linear in ys, w and x, so a difference quotient of any step
     # has no truncation error: only FP32 rounding (about sqrt(n) 2^-24)
