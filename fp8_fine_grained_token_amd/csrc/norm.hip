@@ -333,7 +333,8 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs a) {
 // (kGiven); the rest needs nothing of other columns, so a workgroup then takes
 // a stretch of columns.
 // Within a gate row, dg = b w1 sum D yh and its part of dw1 = b g sum D yh, so
-// one running sum (of D yh) serves both until the gate row ends.
+// one running sum (of D yh) serves both until the gate row ends; where members
+// share gate rows it is their partial row, and the factors come after the sums.
 struct GradPlan {
     int64_t per_gate;   // rows of a gate row
     int64_t run;        // rows of a member
@@ -360,8 +361,7 @@ GradPlan grad_plan(int64_t T, int64_t gate_rows, int64_t most) {
 template <typename B, bool kGiven>
 __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradPlan p, int tx,
                                                                const float2 *given,
-                                                               float *part_post, float *part_pre,
-                                                               float *part_gate) {
+                                                               float *part_post, float *part_pre) {
     using Y = typename B::Y;
     using S = typename B::S;
     constexpr int kVecs = B::vecs;
@@ -446,6 +446,10 @@ __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradP
             load_param<B::narrow>(a.gate, a.param_bf16, gate_row * a.H, span[j], w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[j][i] *= a.branch_scale;
+            if (p.chunks > 1) {  // this member's only gate row
+                if (a.dw_post || a.dgate) store_span(part_post + member * a.H, span[j], acc[j]);
+                continue;
+            }
             if (a.dw_post) {
                 float *part = part_post + member * a.H, sum[8] = {};
                 if (!first_gate) {
@@ -461,8 +465,7 @@ __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradP
                 load_param<B::narrow>(post_weights, a.param_bf16, 0, span[j], w);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) acc[j][i] *= w[i];
-                store_span(p.chunks == 1 ? a.dgate + gate_row * a.H : part_gate + member * a.H,
-                           span[j], acc[j]);
+                store_span(a.dgate + gate_row * a.H, span[j], acc[j]);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[j][i] = 0;
@@ -583,19 +586,29 @@ __global__ __launch_bounds__(1024) void norm_grad_sums_kernel(NormArgs a, float2
     }
 }
 
-// out[group][h] = sum over the group's `rows` partial rows: 64 columns a
+// Each group's `rows` partial rows added: out[group] = p * sum, and with a
+// second output out2[group] = p2 * sum (p, p2 [H], ones without); with `each`
+// [rows / each_rows][H] out = sum of each[row / each_rows] * row.  64 columns a
 // workgroup, 16 threads a column, each every 16th row.
 struct ReduceJob {
     const float *part;
-    float *out;
-    int64_t rows, groups;
+    int rows, each_rows;
+    int64_t groups;
+    const void *each, *p, *p2;
+    float *out, *out2;
 };
 
 struct ReduceJobs {
     ReduceJob job[3];
 };
 
-__global__ __launch_bounds__(1024) void reduce_rows_kernel(ReduceJobs jobs, int64_t H) {
+__device__ __forceinline__ float param_at(const void *p, bool bf16, int64_t i) {
+    if (!p) return 1.0f;
+    return bf16 ? to_float(static_cast<const Bf16 *>(p)[i]) : static_cast<const float *>(p)[i];
+}
+
+__global__ __launch_bounds__(1024) void reduce_rows_kernel(ReduceJobs jobs, int64_t H,
+                                                           bool param_bf16) {
     __shared__ float lds[16][64];
     const ReduceJob job = jobs.job[blockIdx.y];
     const int64_t tiles = (H + 63) / 64;
@@ -605,15 +618,24 @@ __global__ __launch_bounds__(1024) void reduce_rows_kernel(ReduceJobs jobs, int6
         float sum = 0;
         if (h < H) {
             const float *p = job.part + group * job.rows * H + h;
+            if (job.each) {
+#pragma unroll 4
+                for (int r = part; r < job.rows; r += 16)
+                    sum = __builtin_fmaf(
+                        param_at(job.each, param_bf16, r / job.each_rows * H + h), p[r * H], sum);
+            } else {
 #pragma unroll 8
-            for (int64_t r = part; r < job.rows; r += 16) sum += p[r * H];
+                for (int r = part; r < job.rows; r += 16) sum += p[r * H];
+            }
         }
         lds[part][threadIdx.x & 63] = sum;
         __syncthreads();
         if (part == 0 && h < H) {
             sum = 0;
             for (int k = 0; k < 16; ++k) sum += lds[k][threadIdx.x & 63];
-            job.out[group * H + h] = sum;
+            job.out[group * H + h] = param_at(job.p, param_bf16, h) * sum;
+            if (job.out2)
+                job.out2[group * H + h] = param_at(job.p2, param_bf16, h) * sum;
         }
         __syncthreads();
     }
@@ -694,8 +716,7 @@ hipError_t launch_norm_residual(const NormArgs &a, hipStream_t stream) {
 size_t norm_grad_workspace_bytes(int64_t T, int64_t H, int64_t gate_rows) {
     if (T == 0 || H == 0) return 0;
     const GradPlan p = grad_plan(T, gate_rows, grad_members(H));
-    return ((size_t)(p.chunks > 1 ? 3 : 2) * p.members * H + (H > kHeldGrad ? 2 * T : 0)) *
-           sizeof(float);
+    return ((size_t)2 * p.members * H + (H > kHeldGrad ? 2 * T : 0)) * sizeof(float);
 }
 
 hipError_t launch_norm_residual_grad(const NormArgs &a, hipStream_t stream) {
@@ -706,7 +727,7 @@ hipError_t launch_norm_residual_grad(const NormArgs &a, hipStream_t stream) {
     // wide rows' coefficients first: two floats a row, 16-byte aligned
     float2 *given = reinterpret_cast<float2 *>(a.workspace);
     float *part_post = a.workspace + (wide ? 2 * a.T : 0);
-    float *part_pre = part_post + p.members * a.H, *part_gate = part_pre + p.members * a.H;
+    float *part_pre = part_post + p.members * a.H;
     if (a.T > 0) {
         const int64_t per = s.small ? kSmallThreads / s.tx : 1;
         const unsigned blocks = (unsigned)((p.members + per - 1) / per);
@@ -715,14 +736,14 @@ hipError_t launch_norm_residual_grad(const NormArgs &a, hipStream_t stream) {
             using S = decltype(r);
             auto go = [&](auto b) {
                 norm_grad_kernel<decltype(b), false><<<blocks, s.block, 0, stream>>>(
-                    a, p, s.tx, nullptr, part_post, part_pre, part_gate);
+                    a, p, s.tx, nullptr, part_post, part_pre);
             };
             if (wide) {
                 const unsigned rows = (unsigned)(a.T < 2048 ? a.T : 2048);
                 norm_grad_sums_kernel<Y, S><<<rows, 1024, 0, stream>>>(a, given);
                 const dim3 grid(blocks, (unsigned)((a.H + 8 * 256 - 1) / (8 * 256)));
                 norm_grad_kernel<Build<Y, S, 1, 256, false, false>, true>
-                    <<<grid, 256, 0, stream>>>(a, p, 256, given, part_post, part_pre, part_gate);
+                    <<<grid, 256, 0, stream>>>(a, p, 256, given, part_post, part_pre);
             } else if (a.H < 8) {
                 go(Build<Y, S, 1, kSmallThreads, true, true>{});
             } else if (s.small) {
@@ -740,16 +761,36 @@ hipError_t launch_norm_residual_grad(const NormArgs &a, hipStream_t stream) {
     }
     ReduceJobs jobs = {};
     int n = 0;
-    if (a.dw_post) jobs.job[n++] = {part_post, a.dw_post, p.members, 1};
-    if (a.dw_pre) jobs.job[n++] = {part_pre, a.dw_pre, p.members, 1};
-    if (a.dgate && (p.chunks > 1 || a.T == 0))
-        jobs.job[n++] = {part_gate, a.dgate, a.T ? p.chunks : 0, a.gate_rows};
+    auto add = [&](const float *part, int64_t rows, int64_t groups, const void *param,
+                   float *out) -> ReduceJob & {
+        jobs.job[n] = {part, (int)rows, 1, groups, nullptr, param, nullptr, out, nullptr};
+        return jobs.job[n++];
+    };
+    const void *w_post = a.post ? a.w_post : nullptr;
+    if (p.chunks == 1) {  // partial rows of dw_post; dgate is written, but for no tokens
+        if (a.dw_post) add(part_post, p.members, 1, nullptr, a.dw_post);
+        if (a.dgate && a.T == 0) add(part_post, 0, a.gate_rows, nullptr, a.dgate);
+    } else if (a.dw_post && a.dgate && a.gate_rows == 1) {
+        ReduceJob &both = add(part_post, p.members, 1, a.gate, a.dw_post);
+        both.p2 = w_post;
+        both.out2 = a.dgate;
+    } else {
+        if (a.dw_post && a.gate_rows == 1) {
+            add(part_post, p.members, 1, a.gate, a.dw_post);
+        } else if (a.dw_post) {
+            ReduceJob &job = add(part_post, p.members, 1, nullptr, a.dw_post);
+            job.each = a.gate;
+            job.each_rows = (int)p.chunks;
+        }
+        if (a.dgate) add(part_post, p.chunks, a.gate_rows, w_post, a.dgate);
+    }
+    if (a.dw_pre) add(part_pre, p.members, 1, nullptr, a.dw_pre);
     if (n == 0) return hipSuccess;
     int64_t most = 1;
     for (int i = 0; i < n; ++i) most = jobs.job[i].groups > most ? jobs.job[i].groups : most;
     most *= (a.H + 63) / 64;
     const dim3 grid((unsigned)(most < (1 << 20) ? most : (1 << 20)), (unsigned)n);
-    reduce_rows_kernel<<<grid, 1024, 0, stream>>>(jobs, a.H);
+    reduce_rows_kernel<<<grid, 1024, 0, stream>>>(jobs, a.H, a.param_bf16);
     return hipGetLastError();
 }
 
