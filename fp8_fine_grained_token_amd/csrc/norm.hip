@@ -602,13 +602,13 @@ struct ReduceJobs {
     ReduceJob job[3];
 };
 
-__device__ __forceinline__ float param_at(const void *p, bool bf16, int64_t i) {
-    if (!p) return 1.0f;
-    return bf16 ? to_float(static_cast<const Bf16 *>(p)[i]) : static_cast<const float *>(p)[i];
+template <typename P>
+__device__ __forceinline__ float param_at(const void *p, int64_t i) {
+    return p ? to_float(static_cast<const P *>(p)[i]) : 1.0f;
 }
 
-__global__ __launch_bounds__(1024) void reduce_rows_kernel(ReduceJobs jobs, int64_t H,
-                                                           bool param_bf16) {
+template <typename P>
+__global__ __launch_bounds__(1024) void reduce_rows_kernel(ReduceJobs jobs, int64_t H) {
     __shared__ float lds[16][64];
     const ReduceJob job = jobs.job[blockIdx.y];
     const int64_t tiles = (H + 63) / 64;
@@ -619,10 +619,14 @@ __global__ __launch_bounds__(1024) void reduce_rows_kernel(ReduceJobs jobs, int6
         if (h < H) {
             const float *p = job.part + group * job.rows * H + h;
             if (job.each) {
-#pragma unroll 4
+                // row / each_rows by a product: exact, since rows are far below
+                // 2^22 and row + 0.5 is half a row away from any multiple
+                const float per = 1.0f / (float)job.each_rows;
+                const P *each = static_cast<const P *>(job.each) + h;
+#pragma unroll 8
                 for (int r = part; r < job.rows; r += 16)
-                    sum = __builtin_fmaf(
-                        param_at(job.each, param_bf16, r / job.each_rows * H + h), p[r * H], sum);
+                    sum = __builtin_fmaf(to_float(each[(int)(((float)r + 0.5f) * per) * H]),
+                                         p[r * H], sum);
             } else {
 #pragma unroll 8
                 for (int r = part; r < job.rows; r += 16) sum += p[r * H];
@@ -633,9 +637,9 @@ __global__ __launch_bounds__(1024) void reduce_rows_kernel(ReduceJobs jobs, int6
         if (part == 0 && h < H) {
             sum = 0;
             for (int k = 0; k < 16; ++k) sum += lds[k][threadIdx.x & 63];
-            job.out[group * H + h] = param_at(job.p, param_bf16, h) * sum;
+            job.out[group * H + h] = param_at<P>(job.p, h) * sum;
             if (job.out2)
-                job.out2[group * H + h] = param_at(job.p2, param_bf16, h) * sum;
+                job.out2[group * H + h] = param_at<P>(job.p2, h) * sum;
         }
         __syncthreads();
     }
@@ -790,7 +794,8 @@ hipError_t launch_norm_residual_grad(const NormArgs &a, hipStream_t stream) {
     for (int i = 0; i < n; ++i) most = jobs.job[i].groups > most ? jobs.job[i].groups : most;
     most *= (a.H + 63) / 64;
     const dim3 grid((unsigned)(most < (1 << 20) ? most : (1 << 20)), (unsigned)n);
-    reduce_rows_kernel<<<grid, 1024, 0, stream>>>(jobs, a.H, a.param_bf16);
+    auto *kernel = a.param_bf16 ? reduce_rows_kernel<Bf16> : reduce_rows_kernel<float>;
+    kernel<<<grid, 1024, 0, stream>>>(jobs, a.H);
     return hipGetLastError();
 }
 
