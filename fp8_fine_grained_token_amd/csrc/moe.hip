@@ -440,9 +440,12 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(GatherArgs a, Row
 // all ids in L2, so there is no launch between the sort and the gather and
 // nothing to wait for.  One more row of workgroups writes the offsets.  Worth
 // it as long as the ids read in all stay few: 256 tokens of 7168 values to 8
-// experts (2 million ids) 11.3 us against 12.0 in three launches, 512 tokens
-// (8 million) 26 us against 18.
+// experts (2 million ids) 9.5 us against 12 in two launches; 512 tokens (8
+// million) 18 us in them against 26, as measured with one id a lane at a time.
 constexpr int64_t kFewSlots = 4096, kFewReads = (int64_t)1 << 22;
+// Ids a lane reads at a time (256 tokens: 10.9 us with one, 9.5 with four; 512
+// tokens of 2048 values 11.4 and 8.2).
+constexpr int kRound = 4;
 
 template <typename M, typename Id>
 __global__ __launch_bounds__(kRowThreads) void sort_dispatch_kernel(
@@ -503,12 +506,19 @@ __global__ __launch_bounds__(kRowThreads) void sort_dispatch_kernel(
             key[b] = e < 0 ? -1 : e * slots + s;
             count[b] = 0;
         }
-        for (int s0 = wave * 64; s0 < slots; s0 += kRowThreads) {
-            const int s = s0 + lane;
-            const int e = s < slots ? expert_of(ids, s, E) : -1;
-            const int other = e < 0 ? 0x7FFFFFFF : e * slots + s;
+        for (int s0 = wave * 64; s0 < slots; s0 += kRound * kRowThreads) {
+            Id id[kRound];  // one wait for all
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) count[b] += __popcll(__ballot(other < key[b]));
+            for (int i = 0; i < kRound; ++i)
+                id[i] = ids[min(s0 + i * kRowThreads + lane, slots - 1)];
+#pragma unroll
+            for (int i = 0; i < kRound; ++i) {
+                const int s = s0 + i * kRowThreads + lane;
+                const bool kept = s < slots && id[i] >= 0 && id[i] < (Id)E;
+                const int other = kept ? (int)id[i] * slots + s : 0x7FFFFFFF;
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) count[b] += __popcll(__ballot(other < key[b]));
+            }
         }
         __syncthreads();  // the last batch's reads
         if (lane == 0)
