@@ -180,6 +180,23 @@ def test_w4_errors():
     assert grouped(R=0, off=N) == B.FP8_OK
 
 
+def test_widest_rows():
+    # one past the documented limits: expert-ordered rows below 2^28 values,
+    # 4-bit rows below 2^24
+    H, K = 1 << 28, 1 << 24
+    assert call("fp8_moe_combine", A, BF16, H, 8, A, A, 4, 2, H, N, 0, A, BF16,
+                N) == B.FP8_ERR_SHAPE
+    assert call("fp8_moe_combine_grad", A, H, A, H, BF16, 8, A, A, 4, 2, H, A, A,
+                N) == B.FP8_ERR_SHAPE
+    assert call("fp8_moe_dispatch_grad", A, BF16, H, 8, A, 4, 2, H, A, BF16, N) == B.FP8_ERR_SHAPE
+    for suffix in ("", "_pow2"):
+        assert call("fp8_moe_dispatch_quant_1x128" + suffix, A, H, 4, H, A, 2, A, A, 8,
+                    N) == B.FP8_ERR_SHAPE
+    assert call("fp8_w4_matvec", A, K, A, A, 1, 2, 8, K, A, BF16, N) == B.FP8_ERR_SHAPE
+    assert call("fp8_w4_grouped_matvec", A, K, A, A, 1, A, 3, 2, 8, K, A, BF16,
+                N) == B.FP8_ERR_SHAPE
+
+
 # ---- the Python layer: refused before anything is launched ---------------------
 
 def bf(*shape):
