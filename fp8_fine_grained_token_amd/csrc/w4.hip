@@ -97,8 +97,10 @@ __global__ __launch_bounds__(256) void w4_quant_kernel(const uint16_t *__restric
 // row c, the operand of four 16x16x32 products (each takes eight channels of
 // every q, x alike).  Read in operand order, every lane would touch a cache
 // line of its own and the 64 look-ups of a load, not HBM, were the bound (128
-// rows over 32 experts of 4096 x 7168: 131 us).  The next tile's loads are
-// under way while a tile is multiplied.
+// rows over 32 experts of 4096 x 7168, 26 of them with rows: 131 us).  The next
+// tile's loads are under way while a tile is multiplied.  That case takes 93 to
+// 98 us (405 MB of codes and scales, 4.1 to 4.3 TB/s); one row with 2048 x 7168
+// 6.3 us, most of it the launch and one trip to HBM.
 //
 // Few rows leave matrix columns unused, so kSegs of 1, 2 or 4 puts as many
 // stretches of K side by side: the 16 operand rows are then 16 / kSegs rows
@@ -552,7 +554,8 @@ hipError_t launch_w4_matvec(const void *x, int64_t ldx, const void *codes, const
     }
     // Workgroups that can be busy: experts with rows times column tiles.
     // Stretches of K side by side (kSegs) and waves along K (split) both make
-    // more and narrower tiles; they are taken as far as the card needs them.
+    // more and narrower tiles; they are taken as far as the card needs them
+    // (one row: 2048 x 7168 8.0 us without, 6.5 with; 1037 x 1000 9.6 and 4.3).
     const int64_t active = offsets ? (E < R ? E : R) : 1;
     const int64_t want = 256;
     int segs = 1, split_log = 0;
@@ -575,6 +578,12 @@ hipError_t launch_w4_matvec(const void *x, int64_t ldx, const void *codes, const
     p.chunks = (p.blocks + stretches * per - 1) / (stretches * per);
     const int64_t total = groups() / active;  // workgroups of an expert at one step each
     p.steps = 1;
+    // Column tiles of a wave: x is read once for all of them and the next
+    // tile's loads overlap the products, so dense grids stay at one workgroup a
+    // CU (16 rows by 18432 x 7168: 21 us, with 1024 workgroups 32).  Experts
+    // differ in their rows and some have none, so theirs are dealt in smaller
+    // pieces (128 rows over 32 experts of 4096 x 7168: 104 us with 1024, 153
+    // with 256 or 4096).
     const int64_t target = offsets ? 1024 : 256;
     if (total * active > target) p.steps = (int)((total * active + target - 1) / target);
     const dim3 grid((unsigned)((total + p.steps - 1) / p.steps), (unsigned)active);
