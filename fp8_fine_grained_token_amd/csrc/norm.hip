@@ -14,8 +14,8 @@
 // under way while a row's sums are waited for.  The statistics are FP32 sums.
 // 4096 rows of 7168 bf16 values: forward with FP8 result 206 MB in 50 us (4.1
 // TB/s; the two sums a row in series, not HBM, keep it from the 43 us of a
-// copy), gradient 352 MB in 76 to 79 us and 6.6 us for the parameters' sums
-// (4.1 TB/s in all).  One row forward: 6 us, a launch and the chain of load,
+// copy), gradient 352 MB in 70 to 85 us with the 5 us for the parameters' sums
+// (5.0 to 4.1 TB/s, by what the caches hold of the call before).  One row forward: 6 us, a launch and the chain of load,
 // sum, sum, store.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
