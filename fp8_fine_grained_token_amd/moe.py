@@ -13,9 +13,11 @@
 
 As in ``binding``: argument marshalling only, outputs and workspaces are
 allocated when not given, and shapes are checked before anything is launched,
-because the kernels index every buffer by the sizes they are given.  Input
-matrices may have any row stride (``x[:, :h]``, ``x.expand(t, -1)``) as long
-as a row's values are adjacent; everything else must be contiguous.
+because the kernels index every buffer by the sizes they are given; outputs
+and workspaces must not share memory with inputs or each other (but a new
+residual stream or sum may be written over the old one).  Input matrices may
+have any row stride (``x[:, :h]``, ``x.expand(t, -1)``) as long as a row's
+values are adjacent; everything else must be contiguous.
 
 Work goes to ``stream``, or to the current stream of the tensors' device.
 With a ``stream`` of its own, outputs and workspaces are allocated on that
@@ -133,22 +135,43 @@ def _rows(t, name, dtypes, shape=None):
     return t.stride(0)
 
 
-def _disjoint(t, name, others):
-    """Refuse an output whose memory is an input's: the kernels read inputs
-    after they have begun to write outputs."""
-    if t is None:
+def _disjoint(out_names, outputs, in_names, inputs):
+    """Refuse an output (or workspace) whose memory is an input's or another
+    output's: workgroups read inputs while others have begun to write.
+    Tensors or None, the outputs contiguous; names in one string each."""
+    given, top = [], 0
+    for i, t in enumerate(outputs):
+        if t is None:
+            continue
+        a0 = t.data_ptr()
+        a1 = a0 + t.nbytes
+        if a0 == a1:
+            continue
+        for b0, b1, j in given:
+            if a0 < b1 and b0 < a1:
+                _shared(out_names, i, out_names, j)
+        given.append((a0, a1, i))
+        top = a1 if a1 > top else top
+    if not given:
         return
-    a0 = t.data_ptr()
-    a1 = a0 + t.nbytes
-    for other, what in others:
-        # what begins behind the output (or holds nothing) cannot share it
-        if other is None or other.data_ptr() >= a1:
+    for j, t in enumerate(inputs):
+        if t is None:
             continue
-        if other.numel() == 0:
+        b0 = t.data_ptr()
+        if b0 >= top:  # behind every output
             continue
-        span = sum((n - 1) * s for n, s in zip(other.shape, other.stride())) + 1
-        if a0 < other.data_ptr() + span * other.element_size():
-            raise ValueError(f"{name} must not share memory with {what}")
+        size = t.nbytes
+        if size == 0:
+            continue
+        b1 = b0 + (size if t.is_contiguous() else t.element_size() * (
+            1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))))
+        for a0, a1, i in given:
+            if b0 < a1 and a0 < b1:
+                _shared(out_names, i, in_names, j)
+
+
+def _shared(names, i, others, j):
+    raise ValueError(f"{names.split()[i]} must not share memory with {others.split()[j]}")
 
 
 def _plain_empty(shape, strides, dtype):
@@ -280,6 +303,9 @@ def _check_ids(expert_ids, num_experts, group_offsets, slot_row, row_slot, works
     _workspace_tensor(workspace)
 
 
+_PLAN = "group_offsets slot_row row_slot workspace"
+
+
 def _plan(place, expert_ids, num_experts, group_offsets, slot_row, row_slot):
     if group_offsets is None:
         group_offsets = place.empty((num_experts + 1,), torch.int32)
@@ -301,6 +327,7 @@ def fp8_moe_sort(expert_ids, num_experts, group_offsets=None, slot_row=None, row
     (-1 for a dropped slot), row_slot int32 [T k] (-1 past the kept rows))."""
     _check_ids(expert_ids, num_experts, group_offsets, slot_row, row_slot, workspace)
     T, k = expert_ids.shape
+    _disjoint(_PLAN, (group_offsets, slot_row, row_slot, workspace), "expert_ids", (expert_ids,))
     with _Place(stream, "expert_ids group_offsets slot_row row_slot workspace",
                 expert_ids, group_offsets, slot_row, row_slot, workspace) as p:
         plan = _plan(p, expert_ids, num_experts, group_offsets, slot_row, row_slot)
@@ -353,7 +380,7 @@ def fp8_moe_dispatch(x, slot_row, scales=None, xs=None, xs_scales=None, stream=N
             _dense(xs_scales, "xs_scales", (rows, G), _F32)
     elif xs_scales is not None:
         raise ValueError("xs_scales given without scales")
-    _disjoint(xs, "xs", ((x, "x"), (slot_row, "slot_row")))
+    _disjoint("xs xs_scales", (xs, xs_scales), "x slot_row scales", (x, slot_row, scales))
     with _Place(stream, "x slot_row scales xs xs_scales",
                 x, slot_row, scales, xs, xs_scales) as p:
         if xs is None:
@@ -377,6 +404,7 @@ def _dispatch_quant(name, x, slot_row, q, scales, stream):
     rows = q.shape[0] if q is not None else scales.shape[0] if scales is not None else T * k
     if scales is not None:
         _dense(scales, "scales", (rows, G), _F32)
+    _disjoint("q scales", (q, scales), "x slot_row", (x, slot_row))
     with _Place(stream, "x slot_row q scales",
                 x, slot_row, q, scales) as p:
         if q is None:
@@ -410,7 +438,8 @@ def fp8_moe_sort_dispatch(x, expert_ids, num_experts, group_offsets=None, slot_r
         raise ValueError(f"expert_ids must have {T} rows, got {ids_T}")
     if xs is not None:
         _dense(xs, "xs", (T * k, H), (x.dtype,))
-        _disjoint(xs, "xs", ((x, "x"), (expert_ids, "expert_ids")))
+    _disjoint(_PLAN + " xs", (group_offsets, slot_row, row_slot, workspace, xs), "x expert_ids",
+              (x, expert_ids))
     with _Place(stream, "x expert_ids group_offsets slot_row row_slot xs workspace",
                 x, expert_ids, group_offsets, slot_row, row_slot, xs, workspace) as p:
         plan = _plan(p, expert_ids, num_experts, group_offsets, slot_row, row_slot)
@@ -436,6 +465,8 @@ def _sort_dispatch_quant(name, x, expert_ids, num_experts, group_offsets, slot_r
         _dense(q, "q", (T * k, H), _U8)
     if scales is not None:
         _dense(scales, "scales", (T * k, G), _F32)
+    _disjoint(_PLAN + " q scales", (group_offsets, slot_row, row_slot, workspace, q, scales),
+              "x expert_ids", (x, expert_ids))
     with _Place(stream, "x expert_ids group_offsets slot_row row_slot q scales workspace",
                 x, expert_ids, group_offsets, slot_row, row_slot, q, scales, workspace) as p:
         plan = _plan(p, expert_ids, num_experts, group_offsets, slot_row, row_slot)
@@ -481,7 +512,7 @@ def fp8_moe_dispatch_grad(dxs, slot_row, dx=None, out_dtype=None, stream=None):
         dx, torch.Tensor) else dxs.dtype
     if dx is not None:
         _dense(dx, "dx", (T, H), tuple(d for d in _WIDE if d == dtype) or _WIDE)
-        _disjoint(dx, "dx", ((dxs, "dxs"), (slot_row, "slot_row")))
+        _disjoint("dx", (dx,), "dxs slot_row", (dxs, slot_row))
     with _Place(stream, "dxs slot_row dx",
                 dxs, slot_row, dx) as p:
         if dx is None:
@@ -511,10 +542,10 @@ def fp8_moe_combine(ys, slot_row, weights=None, residual=None, out=None, out_dty
         ld_residual = _rows(residual, "residual", (dtype,), (T, H))
     if out is not None:
         _dense(out, "out", (T, H), tuple(d for d in _WIDE if d == dtype) or _WIDE)
-        _disjoint(out, "out", ((ys, "ys"), (slot_row, "slot_row"), (weights, "weights")))
-        if residual is not None and not (residual.data_ptr() == out.data_ptr()
-                                         and ld_residual == H):
-            _disjoint(out, "out", ((residual, "residual (unless it is residual)"),))
+        same = (residual is not None and residual.data_ptr() == out.data_ptr()
+                and ld_residual == H)
+        _disjoint("out", (out,), "ys slot_row weights residual",
+                  (ys, slot_row, weights, None if same else residual))
     with _Place(stream, "ys slot_row weights residual out",
                 ys, slot_row, weights, residual, out) as p:
         if out is None:
@@ -542,10 +573,10 @@ def fp8_moe_combine_grad(dout, ys, slot_row, weights=None, dys=None, dweights=No
         _dense(weights, "weights", (T, k), _F32)
     if dys is not None:
         _dense(dys, "dys", (R, H), (dout.dtype,))
-        _disjoint(dys, "dys", ((dout, "dout"), (ys, "ys"), (slot_row, "slot_row"),
-                               (weights, "weights")))
     if dweights is not None:
         _dense(dweights, "dweights", (T, k), _F32)
+    _disjoint("dys dweights", (dys, dweights), "dout ys slot_row weights",
+              (dout, ys, slot_row, weights))
     with _Place(stream, "dout ys slot_row weights dys dweights",
                 dout, ys, slot_row, weights, dys, dweights) as p:
         if dys is None:
@@ -594,14 +625,8 @@ def _norm(name, quant, y, r, w_post, gate, w_pre, post_norm, residual_scale, bra
     G = (H + 127) // 128
     if r_out is not None:
         _dense(r_out, "r_out", (T, H), (r.dtype,))
-        _disjoint(r_out, "r_out", ((y, "y"), (w_post, "w_post"), (gate, "gate"),
-                                   (w_pre, "w_pre")))
-        if not (r_out.data_ptr() == r.data_ptr() and ldr == H):
-            _disjoint(r_out, "r_out", ((r, "r (unless it is r)"),))
     if n is not None:
         _dense(n, "n", (T, H), (y.dtype,))
-        _disjoint(n, "n", ((y, "y"), (r, "r"), (w_post, "w_post"), (gate, "gate"),
-                           (w_pre, "w_pre")))
     if q is not None:
         _dense(q, "q", (T, H), _U8)
     if scales is not None:
@@ -609,6 +634,9 @@ def _norm(name, quant, y, r, w_post, gate, w_pre, post_norm, residual_scale, bra
     for what, t in (("rstd_post", rstd_post), ("rstd_pre", rstd_pre)):
         if t is not None:
             _dense(t, what, (T,), _F32)
+    same = r_out is not None and r_out.data_ptr() == r.data_ptr() and ldr == H
+    _disjoint("r_out n q scales rstd_post rstd_pre", (r_out, n, q, scales, rstd_post, rstd_pre),
+              "y r w_post gate w_pre", (y, None if same else r, w_post, gate, w_pre))
     with _Place(stream, "y r w_post gate w_pre r_out n q scales rstd_post rstd_pre",
                 y, r, w_post, gate, w_pre, r_out, n, q, scales, rstd_post, rstd_pre) as p:
         if r_out is None:
@@ -700,14 +728,15 @@ def fp8_norm_residual_grad(dn, dr_out, y, r_out, rstd_post, rstd_pre, w_post=Non
     else:
         rstd_post = w_post = None
     code, gate_rows = _norm_params(H, T, w_post, gate, w_pre)
-    read = ((dn, "dn"), (dr_out, "dr_out"), (y, "y"), (r_out, "r_out"))
     if dy is not None:
         _dense(dy, "dy", (T, H), (y.dtype,))
-        _disjoint(dy, "dy", read)
     if dr is not None:
         _dense(dr, "dr", (T, H), (r_out.dtype,))
-        _disjoint(dr, "dr", read + ((dy, "dy"),))
     _workspace_tensor(workspace)
+    _disjoint("dy dr workspace", (dy, dr, workspace),
+              "dn dr_out y r_out rstd_post rstd_pre w_post gate w_pre",
+              (dn, dr_out, y, r_out, rstd_post, rstd_pre if dn is not None else None, w_post, gate,
+               w_pre))
     with _Place(stream, "dn dr_out y r_out rstd_post rstd_pre w_post gate w_pre dy dr workspace",
                 dn, dr_out, y, r_out, rstd_post, rstd_pre, w_post, gate, w_pre, dy, dr,
                 workspace) as p:
@@ -744,6 +773,7 @@ def _w4_quant(name, w, group, scale_type, codes, scales, stream):
         _dense(codes, "codes", code_shape, _U8)
     if scales is not None:
         _dense(scales, "scales", scale_shape, (scale_type,))
+    _disjoint("codes scales", (codes, scales), "w", (w,))
     with _Place(stream, "w codes scales",
                 w, codes, scales) as p:
         if codes is None:
@@ -793,7 +823,7 @@ def fp8_w4_matvec(x, codes, scales, out_dtype="bf16", y=None, stream=None):
     (M, K), N = x.shape, codes.shape[0]
     if y is not None:
         _dense(y, "y", (M, N), (dtype,))
-        _disjoint(y, "y", ((x, "x"), (codes, "codes"), (scales, "scales")))
+        _disjoint("y", (y,), "x codes scales", (x, codes, scales))
     with _Place(stream, "x codes scales y",
                 x, codes, scales, y) as p:
         if y is None:
@@ -815,8 +845,7 @@ def fp8_w4_grouped_matvec(x, codes, scales, group_offsets, out_dtype="bf16", y=N
     _dense(group_offsets, "group_offsets", (E + 1,), _INT)
     if y is not None:
         _dense(y, "y", (R, N), (dtype,))
-        _disjoint(y, "y", ((x, "x"), (codes, "codes"), (scales, "scales"),
-                           (group_offsets, "group_offsets")))
+        _disjoint("y", (y,), "x codes scales group_offsets", (x, codes, scales, group_offsets))
     with _Place(stream, "x codes scales group_offsets y",
                 x, codes, scales, group_offsets, y) as p:
         if y is None:

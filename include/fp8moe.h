@@ -12,6 +12,8 @@
  *     `ld...` in elements (0 repeats one row); outputs, integer inputs, codes
  *     and scales are dense.  Pointers need the alignment of one element (or
  *     what the call states); wider accesses are the kernels' own matter.
+ *   - Outputs and workspaces must not overlap inputs or each other, but where
+ *     a call says so: inputs are still read when outputs are begun.
  *   - NaN and infinities propagate as the formulas have it; in a dropped slot
  *     nothing is read at all, so whatever stands there has no effect.
  *   - Sums, norms and products are FP32; an output is rounded once, to
