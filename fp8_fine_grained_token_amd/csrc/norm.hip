@@ -61,7 +61,9 @@ __device__ __forceinline__ const T *in_row(const void *p, int64_t row_at, const 
     return span_at(static_cast<const T *>(p) + row_at, s);
 }
 
-// A parameter's values of a span (ones without one).
+// A parameter's values of a span (ones without one), zeros in columns that are
+// not the span's own: the row's values are zero there, and an infinite
+// parameter times them would put NaN into the sums.
 template <bool kNarrow>
 __device__ __forceinline__ void load_param(const void *p, bool bf16, int64_t at, const Span &s,
                                            float (&f)[8]) {
@@ -71,11 +73,11 @@ __device__ __forceinline__ void load_param(const void *p, bool bf16, int64_t at,
     } else if (bf16) {
         Raw8<Bf16> r;
         load_raw<kNarrow>(in_row<Bf16>(p, at, s), s.hi, r);
-        unpack(r, f);
+        unpack_own(r, s, f);
     } else {
         Raw8<float> r;
         load_raw<kNarrow>(in_row<float>(p, at, s), s.hi, r);
-        unpack(r, f);
+        unpack_own(r, s, f);
     }
 }
 
