@@ -529,8 +529,12 @@ __global__ __launch_bounds__(B::threads) void norm_grad_kernel(NormArgs a, GradP
                 const float D = __builtin_fmaf(-c1, rh[j][i], e[j][i]);
                 dr[i] = a.residual_scale * D;
                 acc[j][i] = __builtin_fmaf(D, yh[j][i], acc[j][i]);
-                dy[i] = rs1 * (D * qv[i] - yh[j][i] * c2);
+                dy[i] = D * qv[i];
             }
+            // (without the first norm y is not in dy at all, be it infinite)
+            if (a.post)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dy[i] = rs1 * (dy[i] - yh[j][i] * c2);
             store_span(static_cast<S *>(a.dr) + t * a.H, span[j], dr);
             store_span(static_cast<Y *>(a.dy) + t * a.H, span[j], dy);
         }

@@ -55,3 +55,30 @@ def test_infinite_parameter_is_counted_once(H, bad):
         assert r_out[:, at].isinf().all() and n[:, at].isnan().all()
         r_out[:, at] = n[:, at] = 0
         assert r_out.isfinite().all() and not n.any()
+
+
+@pytest.mark.parametrize("bad", [INF, NAN])
+@pytest.mark.parametrize("H", [5, 300, 2500, 9000])
+def test_gradient_without_post_norm_is_blind_to_y(H, bad):
+    # y enters only the gate's gradient, in its own column
+    t = torch()
+    T = 6
+    y, dn = draw(1, (T, H)), draw(2, (T, H))
+    r_out, dr_out = draw(3, (T, H), "f32"), draw(4, (T, H), "f32")
+    gate, w = draw(5, (H,), "f32", 0.3, 1.0), draw(6, (H,), "f32", 0.1, 1.0)
+    rstd = 1 / r_out.square().mean(1).sqrt()
+
+    def grad(dn, dr_out):
+        return M.fp8_norm_residual_grad(dn, dr_out, y, r_out, None, rstd, None, gate, w,
+                                        post_norm=False, branch_scale=0.7)
+
+    for which in ((dn, dr_out), (None, dr_out), (dn, None)):
+        y[2, H // 2] = 1.0
+        clean = grad(*which)
+        y[2, H // 2] = bad
+        got = grad(*which)
+        for name, a, b in zip(("dy", "dr", "dw_post", "dgate", "dw_pre"), got, clean):
+            if name == "dgate":
+                assert not a[H // 2].isfinite()
+                a[H // 2] = b[H // 2]
+            assert (a is None and b is None) or t.equal(a, b), name
