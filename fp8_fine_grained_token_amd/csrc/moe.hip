@@ -393,7 +393,7 @@ __device__ __forceinline__ void quant_vecs(const GatherArgs &a, int64_t t, int64
     for (int i = 0; i < M::vecs; ++i) {
         float f[8];
         unpack_own(raw[i], s[i], f);
-        bytes[i] = quantize8(f, row16_max(absmax8(f)), s[i].any(), M::pow2, scale[i]);
+        bytes[i] = quantize8(f, group_max(f), s[i].any(), M::pow2, scale[i]);
     }
     for (int64_t j0 = 0; j0 < a.k; j0 += kBatch) {
         int32_t rows[kBatch];

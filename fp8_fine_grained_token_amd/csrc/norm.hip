@@ -237,7 +237,7 @@ __global__ __launch_bounds__(B::threads, B::waves) void norm_kernel(NormArgs a, 
             if (a.n) store_span(static_cast<Y *>(a.n) + t * a.H, span[j], s[j]);
             if (kQuant) {
                 float scale;
-                const uint2 bytes = quantize8(s[j], row16_max(absmax8(s[j])), span[j].any(),
+                const uint2 bytes = quantize8(s[j], group_max(s[j]), span[j].any(),
                                               a.pow2, scale);
                 store_e4m3(static_cast<uint8_t *>(a.q) + t * a.H, span[j], bytes);
                 if ((lane & 15) == 0 && span[j].any())
@@ -318,7 +318,7 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs a) {
             if (kQuant) {
                 float scale;
                 const uint2 bytes =
-                    quantize8(s, row16_max(absmax8(s)), span.any(), a.pow2, scale);
+                    quantize8(s, group_max(s), span.any(), a.pow2, scale);
                 store_e4m3(static_cast<uint8_t *>(a.q) + t * a.H, span, bytes);
                 if ((threadIdx.x & 15) == 0 && span.any()) a.scales[t * G + v / 16] = scale;
             }

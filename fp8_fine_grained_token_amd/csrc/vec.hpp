@@ -168,13 +168,33 @@ __device__ __forceinline__ void store_span(float *row, const Span &s, const floa
             if (s.has(i)) span_at(row, s)[i] = f[i];
     }
 }
-// E4M3 bytes and scale of a lane's part of a 1x128 group of maximum `amax`
+
+// Largest magnitude of the 1x128 group that 16 lanes hold, as bits: of bits, a
+// maximum keeps NaN (above infinity, above every number), which fmaxf drops.
+__device__ __forceinline__ uint32_t group_max(const float (&f)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+    // over the 16 lanes, in the steps of row16_max
+    m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true));
+    m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true));
+    m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x141, 0xF, 0xF, true));
+    m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x140, 0xF, 0xF, true));
+    return m;
+}
+
+// E4M3 bytes and scale of a lane's part of a 1x128 group of maximum `bits`
 // (`used`: the lane holds any of it).  The usual groups take a path without
 // branches and with one divide (the activation quantizer's); a wave with an
-// all-zero or tiny group takes the general one.
-__device__ __forceinline__ uint2 quantize8(const float (&f)[8], float amax, bool used, bool pow2,
+// all-zero, tiny or non-finite group takes the general one.  A group that
+// holds a NaN or an infinity reads back as NaN: the scale is its maximum and
+// the codes are E4M3's NaN.
+__device__ __forceinline__ uint2 quantize8(const float (&f)[8], uint32_t bits, bool used, bool pow2,
                                            float &scale) {
-    if (__all(!used || (pow2 ? amax > 0.0f : amax >= 0x1p-60f))) {
+    constexpr uint32_t kInf = 0x7F800000u, kTiny = 0x21800000u;  // 2^-60
+    const float amax = __uint_as_float(bits);
+    const uint32_t least = pow2 ? 1 : kTiny;
+    if (__all(!used || bits - least < kInf - least)) {
         scale = pow2 ? scale_pow2(amax) : scale_fast(amax);
         const float r = 1.0f / scale;
         uint32_t lo = 0, hi = 0;
@@ -184,6 +204,8 @@ __device__ __forceinline__ uint2 quantize8(const float (&f)[8], float amax, bool
         hi = cvt_pk_e4m3<true>(quot_fast(f[6], scale, r), quot_fast(f[7], scale, r), hi);
         return make_uint2(lo, hi);
     }
+    scale = amax;
+    if (bits >= kInf) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
     const QuotientCtx qc(amax, pow2);
     scale = qc.s;
     return quant8(f, qc);

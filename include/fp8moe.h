@@ -14,8 +14,12 @@
  *     what the call states); wider accesses are the kernels' own matter.
  *   - Outputs and workspaces must not overlap inputs or each other, but where
  *     a call says so: inputs are still read when outputs are begun.
- *   - NaN and infinities propagate as the formulas have it; in a dropped slot
- *     nothing is read at all, so whatever stands there has no effect.
+ *   - NaN and infinities propagate as the formulas have it (fp8blk.h leaves
+ *     them out of its contract; here they are in it); in a dropped slot
+ *     nothing is read at all, so whatever stands there has no effect.  A 1x128
+ *     group that holds one is quantized so that it reads back as NaN: its
+ *     scale is the largest magnitude (NaN, else infinity), with power-of-two
+ *     scales too, and its codes are NaN.
  *   - Sums, norms and products are FP32; an output is rounded once, to
  *     nearest even.  Results do not depend on the run: no sum uses
  *     floating-point atomics.
@@ -74,7 +78,7 @@ fp8_status fp8_moe_dispatch(const void *x, int elem_bytes, int64_t ldx, const fl
 /*
  * The same with the 1x128 quantizer in the gather: q[row], scales[row] are
  * the E4M3 bytes and scales fp8_quant_act_1x128 (or its _pow2 form) gives for
- * x[t]; each token is read and quantized once.
+ * a finite x[t]; each token is read and quantized once.
  *   x_bf16 [T][H] bf16; q [R][H]; scales [R][ceil(H/128)]
  */
 fp8_status fp8_moe_dispatch_quant_1x128(const void *x_bf16, int64_t ldx, int64_t T, int64_t H,

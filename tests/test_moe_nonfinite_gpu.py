@@ -82,3 +82,71 @@ def test_gradient_without_post_norm_is_blind_to_y(H, bad):
                 assert not a[H // 2].isfinite()
                 a[H // 2] = b[H // 2]
             assert (a is None and b is None) or t.equal(a, b), name
+
+
+def check_quantized(x, q, s, q0, s0, bad_groups, rows):
+    """Groups of `rows` ([slots] -> row) of x: NaN or infinite scale and NaN
+    read back for the (token, group) pairs of bad_groups, every other group
+    equal to the clean call's (q0, s0)."""
+    q, s, q0, s0 = host(q).copy(), host(s).copy(), host(q0), host(s0)
+    nan_code = (np.arange(256) & 0x7F) == 0x7F
+    for tok, g, want in bad_groups:
+        for r in rows[tok]:
+            at = slice(128 * g, min(128 * g + 128, q.shape[1]))
+            assert np.isnan(s[r, g]) if np.isnan(want) else s[r, g] == INF, (tok, g, s[r, g])
+            codes = q[r, at]
+            with np.errstate(invalid="ignore"):
+                back = np.where(nan_code[codes], NAN, e4m3_lut()[codes]) * s[r, g]
+            assert np.isnan(back).all(), (tok, g, codes)
+            q[r, at], s[r, g] = q0[r, at], s0[r, g]
+    assert np.array_equal(q, q0) and np.array_equal(s.view(np.uint32), s0.view(np.uint32))
+
+
+# the last one takes several vectors a thread
+@pytest.mark.parametrize("suffix", ["", "_pow2"])
+@pytest.mark.parametrize("T,k,H", [(1, 2, 1001), (9, 3, 5), (40, 2, 640), (4200, 2, 1001)])
+def test_gather_keeps_nonfinite_groups(T, k, H, suffix):
+    t = torch()
+    E, G = 4, (H + 127) // 128
+    ids = cuda(np.random.default_rng(T).integers(0, E, (T, k)))
+    _, slot_row, _ = M.fp8_moe_sort(ids, E)
+    x = draw(H, (T, H))
+    if T > 2:
+        x[1] = 0  # an all-zero row beside them
+    rows = host(slot_row)
+    tok = min(2, T - 1)
+    bad = [(tok, 0, NAN), (tok, G - 1, INF)] if G > 1 else [(tok, 0, NAN)]
+    gather = getattr(M, "fp8_moe_dispatch_quant_1x128" + suffix)
+    both = getattr(M, "fp8_moe_sort_dispatch_quant_1x128" + suffix)
+    q0, s0 = gather(x, slot_row)
+    for put in (NAN, -NAN):
+        x[tok, 3] = put
+        if G > 1:
+            x[tok, H - 2] = -INF
+        q, s = gather(x, slot_row)
+        check_quantized(x, q, s, q0, s0, bad, rows)
+        _, _, _, q, s = both(x, ids, E)
+        check_quantized(x, q, s, q0, s0, bad, rows)
+    x[tok, 3] = INF
+    q, s = gather(x, slot_row)
+    check_quantized(x, q, s, q0, s0, [(tok, 0, INF)] + bad[1:], rows)
+    assert t.equal(both(x, ids, E)[4], s)
+
+
+@pytest.mark.parametrize("suffix", ["", "_pow2"])
+@pytest.mark.parametrize("H,back", [(5, 2), (300, 2), (1001, 2), (1027, 6), (7168, 2), (16387, 6)])
+def test_norm_keeps_nonfinite_groups(H, back, suffix):
+    # a weight of the second norm: one group of every row (with `back` 6 a group
+    # whose last columns the next group's only vector reads too)
+    T, at = 3, H - back
+    y, r = draw(1, (T, H)), draw(2, (T, H), "f32")
+    w = draw(3, (H,), "f32", 0.1, 1.0)
+    quant = getattr(M, "fp8_norm_residual_quant_1x128" + suffix)
+    r0, q0, s0, _, rs0 = quant(y, r, None, None, w)
+    for put in (NAN, INF):
+        bad = w.clone()
+        bad[at] = put
+        r1, q, s, _, rs = quant(y, r, None, None, bad)
+        assert torch().equal(r1, r0) and torch().equal(rs, rs0)
+        check_quantized(None, q, s, q0, s0, [(i, at // 128, put) for i in range(T)],
+                        [[i] for i in range(T)])
