@@ -239,8 +239,12 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
     };
 
     // Byte offsets of this lane's 16 bytes of each load within a tile (K below
-    // 2^24 keeps them in 32 bits), and of its scale words.
+    // 2^24 keeps them in 32 bits), and of its scale words.  A block past the
+    // row's last takes the last one's scales.
     uint32_t code_at[kPer], scale_at[kScaleLoads];
+    auto scale_word = [&](int j, int chunk) {
+        return min(first_block(j / kPer, chunk) + j % kPer, p.blocks - 1);
+    };
     auto place = [&](int chunk) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -252,14 +256,15 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
         for (int i = 0; i < kScaleLoads; ++i) {
             const int j = min(64 * i + lane, 16 * kPer - 1), r = j / kPer;
             const int n = min(r % kCols, (int)(p.N < 16 ? p.N : 16) - 1);
-            scale_at[i] = n * (uint32_t)scale_bytes + (first_block(r, chunk) + j % kPer) * 4u;
+            scale_at[i] = n * (uint32_t)scale_bytes + scale_word(j, chunk) * 4u;
         }
     };
     u32x4 code[kPer];
     uint32_t scale[kScaleLoads];
     // What lies past the end of a row (and in blocks past its last one) meets
     // zeros of x, so only a read past the end of the whole array is avoided:
-    // it begins earlier and is moved down before it is used.
+    // it begins earlier and is moved down before it is used.  Scales are the
+    // row's own in every case: another's need not be finite.
     auto near_end = [&](int64_t tile) {
         return (e * p.N + first_column(tile) + kCols) * row_bytes + 64ll * kPer * stretches * p.chunks
                    > p.E * p.N * row_bytes;
@@ -290,6 +295,8 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
                 scale[i] = *reinterpret_cast<const u32_any *>(scale_from + scale_at[i]);
         }
     };
+    // Of a row's last word of E8M0 bytes, those that are not the next row's.
+    const uint32_t own_bytes = scale_bytes % 4 ? (1u << 8 * (scale_bytes % 4)) - 1 : ~0u;
     // Loaded registers to the wave's LDS.
     auto keep_tile = [&](int64_t tile) {
         if (near_end(tile)) {
@@ -379,11 +386,12 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
 
         f32x4 acc = {0, 0, 0, 0};
         int buffer = 0;
-        auto products = [&] {
+        auto products = [&](int chunk) {
 #pragma unroll
             for (int b = 0; b < kPer; ++b) {
                 const u32x4 code = my_codes[4 * kPer * c + 4 * b + q];
-                const uint32_t word = my_scales[kPer * c + b];
+                uint32_t word = my_scales[kPer * c + b];
+                if (kE8m0) word &= first_block(c, chunk) + b >= p.blocks - 1 ? own_bytes : ~0u;
                 const float s = __uint_as_float(kE8m0 ? (word >> (8 * q) & 0xFF) << 23 : word);
                 bf16x8 w[4];
 #pragma unroll
@@ -441,6 +449,7 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
         for (int64_t u = 0; u < units; ++u) {
             keep_tile(tile);
             const int64_t done = tile;
+            const int done_chunk = chunk;
             if (u + 1 < units) {
                 if (kChunked) {
                     chunk = chunk + 1 < p.chunks ? chunk + 1 : 0;
@@ -449,7 +458,7 @@ __global__ __launch_bounds__(64 * kWaves) void w4_matvec_kernel(
                 if (!kChunked || chunk == 0) tile += tiles_each;
                 load_tile(tile);
             }
-            products();
+            products(done_chunk);
             if (kChunked && u + 1 < units) load_x(chunk);
             if (!kChunked || chunk == 0 || u + 1 == units) store(done);
         }

@@ -243,8 +243,9 @@ fp8_status fp8_w4_quant_1x32(const void *w_bf16, int64_t N, int64_t K, void *cod
  * (decoding); any M is right, 16 rows at a pass over the weights.
  *   x_bf16 [M][K] bf16, used as it is (products are exact in fp32)
  *   y      [M][N] of out_dtype
- * K < 2^24 (FP8_ERR_SHAPE); K = 0 gives zeros.  Scales must be finite (E8M0:
- * codes up to 252, so that no weight overflows).
+ * K < 2^24 (FP8_ERR_SHAPE); K = 0 gives zeros.  A weight of 2^128 or more (E8M0
+ * bytes 253 and 254 have some) is infinite and E8M0 byte 255 is NaN; a scale
+ * that is not finite shows in its row's output alone.
  */
 fp8_status fp8_w4_matvec(const void *x_bf16, int64_t ldx, const void *codes, const void *scales,
                          int scale_kind, int64_t M, int64_t N, int64_t K, void *y,

@@ -150,3 +150,60 @@ def test_norm_keeps_nonfinite_groups(H, back, suffix):
         assert torch().equal(r1, r0) and torch().equal(rs, rs0)
         check_quantized(None, q, s, q0, s0, [(i, at // 128, put) for i in range(T)],
                         [[i] for i in range(T)])
+
+
+# K in whole and in part blocks of 128, and more blocks than the waves' parts
+# of a row come to: 300 (3 blocks), 1000, 1100 (9), 5120 (40), 8200 (65)
+@pytest.mark.parametrize("rows", [1, 12])
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+@pytest.mark.parametrize("K", [20, 100, 300, 1000, 1100, 2300, 5120, 8200])
+def test_a_nonfinite_scale_stays_in_its_output(K, kind, rows):
+    t = torch()
+    N, group = 70, 128 if kind == "f32" else 32
+    rng = np.random.default_rng(K)
+    codes = cuda(rng.integers(0, 256, (N, (K + 1) // 2), dtype=np.uint8))
+    G = (K + group - 1) // group
+    if kind == "f32":
+        scales, bads = cuda(rng.random((N, G), dtype=np.float32) + 0.5), (NAN, INF, -INF)
+    else:
+        scales, bads = cuda(rng.integers(120, 130, (N, G), dtype=np.uint8)), (255,)
+    x = draw(K, (rows, K))
+    clean = M.fp8_w4_matvec(x, codes, scales, out_dtype="f32")
+    w3, c3 = t.stack([codes] * 3), t.stack([scales] * 3)
+    off = t.tensor([0, 0, rows, rows], dtype=t.int32, device="cuda")
+    for bad in bads:
+        s = scales.clone()
+        s[10] = s[33, 0] = bad
+        y = M.fp8_w4_matvec(x, codes, s, out_dtype="f32")
+        assert not y[:, [10, 33]].isfinite().any()
+        y[:, [10, 33]] = clean[:, [10, 33]]
+        assert t.equal(y, clean)
+        # the experts on both sides
+        s3 = c3.clone()
+        s3[0] = s3[2] = bad
+        assert t.equal(M.fp8_w4_grouped_matvec(x, w3, s3, off, out_dtype="f32"), clean)
+
+
+@pytest.mark.parametrize("K,N", [(6, 2), (64, 40), (1000, 40), (8200, 24)])
+def test_ends_of_the_e8m0_range(K, N):
+    # one-hot rows of x read single weights; x keeps the product in range.
+    # Low bytes: weights down to 2^-128, subnormal in bf16 and fp32.
+    t = torch()
+    rng = np.random.default_rng(K)
+    value = np.array([0, .5, 1, 1.5, 2, 3, 4, 6, -0., -.5, -1, -1.5, -2, -3, -4, -6])
+    at = rng.choice(K, min(K, 16), replace=False)
+    for byte, far in ((0, 90), (1, 90), (2, 90), (250, -90), (251, -90), (252, -90), (253, -90),
+                      (254, -90)):
+        c = rng.integers(0, 16, (N, K + K % 2))
+        if byte > 252:  # weights below 2^128: up to 3 2^126, 1.5 2^127
+            c = np.where((c & 7) > (5 if byte == 253 else 3), c & 8, c)
+        packed = (c[:, 0::2] | c[:, 1::2] << 4).astype(np.uint8)
+        scales = np.full((N, (K + 31) // 32), byte, np.uint8)
+        x = t.zeros((at.size, K), dtype=t.bfloat16, device="cuda")
+        x[t.arange(at.size), t.from_numpy(at)] = 2.0 ** far
+        y = M.fp8_w4_matvec(x, cuda(packed), cuda(scales), out_dtype="f32")
+        want = value[c[:, at]].T * 2.0 ** (byte - 127 + far)
+        assert np.array_equal(y.double().cpu().numpy(), want), byte
+        if byte > 252:  # 6 * 2^126 and more is past every type
+            packed[5 % N, 0] = 0x77
+            assert not M.fp8_w4_matvec(x, cuda(packed), cuda(scales))[:, 5 % N].isfinite().any()
