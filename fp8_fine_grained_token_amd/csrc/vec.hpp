@@ -169,18 +169,28 @@ __device__ __forceinline__ void store_span(float *row, const Span &s, const floa
     }
 }
 
-// Largest magnitude of the 1x128 group that 16 lanes hold, as bits: of bits, a
-// maximum keeps NaN (above infinity, above every number), which fmaxf drops.
-__device__ __forceinline__ uint32_t group_max(const float (&f)[8]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
-    // over the 16 lanes, in the steps of row16_max
+// The larger of two magnitudes, by their bits: so NaN, which fmaxf drops, is
+// above infinity and infinity above every number.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+__device__ __forceinline__ float max_magnitude(float a, float b) {
+    return __uint_as_float(max(magnitude(a), magnitude(b)));
+}
+
+// The same over the 16 lanes of a DPP row, in the steps of row16_max.
+__device__ __forceinline__ uint32_t row16_max_bits(uint32_t m) {
     m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true));
     m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true));
     m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x141, 0xF, 0xF, true));
     m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x140, 0xF, 0xF, true));
     return m;
+}
+
+// Largest magnitude of the 1x128 group that 16 lanes hold, as bits.
+__device__ __forceinline__ uint32_t group_max(const float (&f)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, magnitude(f[i]));
+    return row16_max_bits(m);
 }
 
 // E4M3 bytes and scale of a lane's part of a 1x128 group of maximum `bits`

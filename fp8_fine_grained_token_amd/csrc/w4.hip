@@ -39,7 +39,8 @@ __global__ __launch_bounds__(256) void w4_quant_kernel(const uint16_t *__restric
         const int64_t k = 128 * g + 2 * lane;
         const float a = k < K ? __uint_as_float((uint32_t)w[n * K + k] << 16) : 0.0f;
         const float b = k + 1 < K ? __uint_as_float((uint32_t)w[n * K + k + 1] << 16) : 0.0f;
-        float amax = row16_max(fmaxf(fabsf(a), fabsf(b)));  // 16 lanes: 32 channels
+        // maxima of bits keep NaN; 16 lanes: 32 channels
+        float amax = __uint_as_float(row16_max_bits(max(magnitude(a), magnitude(b))));
         float qa = 0, qb = 0;
         if (kE8m0) {
             // smallest E with 6 * 2^E >= amax: amax = (1 + f) 2^(e - 127) and
@@ -47,6 +48,7 @@ __global__ __launch_bounds__(256) void w4_quant_kernel(const uint16_t *__restric
             const uint32_t bits = __float_as_uint(amax);
             int E = (int)(bits >> 23) - 129 + ((bits & 0x7FFFFFu) > 0x400000u ? 1 : 0);
             E = E < -127 ? -127 : E;
+            if (bits >= 0x7F800000u) E = 128;  // E8M0's NaN
             // x / 2^E in two exact steps (2^-E itself can leave the range)
             const int h = -E / 2;
             const float r0 = __uint_as_float((uint32_t)(h + 127) << 23);
@@ -57,9 +59,9 @@ __global__ __launch_bounds__(256) void w4_quant_kernel(const uint16_t *__restric
             if ((lane & 15) == 0 && k < K)
                 static_cast<uint8_t *>(scales)[n * ((K + 31) / 32) + group] = (uint8_t)(E + 127);
         } else {
-            amax = fmaxf(amax, __shfl_xor(amax, 16));
-            amax = fmaxf(amax, __shfl_xor(amax, 32));
-            const float s = amax / 6.0f;
+            amax = max_magnitude(amax, __shfl_xor(amax, 16));
+            amax = max_magnitude(amax, __shfl_xor(amax, 32));
+            const float s = amax / 6.0f;  // NaN or infinite with a weight that is
             if (s > 0) {
                 qa = a / s;
                 qb = b / s;

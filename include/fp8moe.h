@@ -231,7 +231,10 @@ typedef enum {
  *          FP8_W4_E8M0_1X32: bytes [N][ceil(K/32)], the smallest power of two
  *          from 2^-127 on that is at least amax / 6
  * code = E2M1 round to nearest even of fl32(w / s); an all-zero group has
- * scale 0 (fp32) or 2^-127 and codes 0.
+ * scale 0 (fp32) or 2^-127 and codes 0.  A group that holds a NaN or an
+ * infinity has scale NaN or infinity (fp32), or the NaN byte 255: products
+ * with its row are NaN.  Weights of 1.75 * 2^127 and more (near the end of
+ * bf16's range) round up to 2^128 with E8M0 scales, and that is infinite.
  */
 fp8_status fp8_w4_quant_1x128(const void *w_bf16, int64_t N, int64_t K, void *codes,
                               float *scales, void *hip_stream);

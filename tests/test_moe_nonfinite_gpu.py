@@ -207,3 +207,48 @@ def test_ends_of_the_e8m0_range(K, N):
         if byte > 252:  # 6 * 2^126 and more is past every type
             packed[5 % N, 0] = 0x77
             assert not M.fp8_w4_matvec(x, cuda(packed), cuda(scales))[:, 5 % N].isfinite().any()
+
+
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+@pytest.mark.parametrize("K", [20, 300, 1000])
+def test_weight_quantizer_marks_nonfinite_groups(K, kind, bad):
+    # the group's scale is NaN or infinite (E8M0: the NaN byte), so that a
+    # product with the row is NaN; the other groups are as ever
+    t = torch()
+    N, group = 40, 128 if kind == "f32" else 32
+    quant = M.fp8_w4_quant_1x128 if kind == "f32" else M.fp8_w4_quant_1x32
+    w = draw(K, (N, K), sigma=0.02)
+    codes0, scales0 = quant(w)
+    g = (K - 1) // group
+    w[7, K - 2] = bad
+    codes, scales = quant(w)
+    if kind == "e8m0":
+        assert int(scales[7, g]) == 255
+    else:
+        assert scales[7, g].isnan() if np.isnan(bad) else scales[7, g] == INF
+    scales[7, g] = scales0[7, g]
+    codes[7, group * g // 2:] = codes0[7, group * g // 2:]
+    assert t.equal(codes, codes0) and t.equal(scales, scales0)
+    x = draw(K + 1, (3, K))
+    x[1] = 0
+    clean = M.fp8_w4_matvec(x, codes0, scales0, out_dtype="f32")
+    y = M.fp8_w4_matvec(x, *quant(w), out_dtype="f32")
+    assert y[:, 7].isnan().all()
+    y[:, 7] = clean[:, 7]
+    assert t.equal(y, clean)
+
+
+def test_weights_at_the_end_of_the_range():
+    # bf16 reaches 1.99 * 2^127: with E8M0 scales 1.75 * 2^127 rounds to 2^128
+    t = torch()
+    w = draw(1, (40, 96))
+    w[3, 40], w[5, 40], w[7, 70] = 1.5 * 2.0 ** 127, 1.73 * 2.0 ** 127, 1.75 * 2.0 ** 127
+    codes, scales = M.fp8_w4_quant_1x32(w)
+    assert scales[[3, 5, 7], [1, 1, 2]].tolist() == [252, 253, 253]
+    x = t.zeros((2, 96), dtype=t.bfloat16, device="cuda")
+    x[0, 40] = 2.0 ** -100
+    y = M.fp8_w4_matvec(x, codes, scales, out_dtype="f32")
+    assert y[0, 3] == y[0, 5] == 1.5 * 2.0 ** 27 and not y[:, 7].isfinite().any()
+    y[:, 7] = 0
+    assert y.isfinite().all()
