@@ -174,8 +174,6 @@ fp8_status w4_matvec(const void *x, int64_t ldx, const void *codes, const void *
         return FP8_ERR_SHAPE;
     if (!stride_ok(R, ldx)) return FP8_ERR_SHAPE;
     if (E < 0 || E > 65535 || N * K >= kMaxElems / (E > 0 ? E : 1)) return FP8_ERR_SHAPE;
-    // a launch holds below 2^32 threads
-    if (((N + 3) / 4) * (E > 0 ? E : 1) >= ((int64_t)1 << 24)) return FP8_ERR_SHAPE;
     if (R == 0 || N == 0) return FP8_OK;
     if (E == 0) return FP8_ERR_SHAPE;
     if (!y || (K > 0 && (!x || !codes || !scales)) || (grouped && !offsets)) return FP8_ERR_NULL;
