@@ -223,8 +223,8 @@ fp8_status fp8_moe_dispatch(const void *x, int elem_bytes, int64_t ldx, const fl
     if (!xs || (x_scales != nullptr) != (xs_scales != nullptr)) return FP8_ERR_NULL;
     if (!aligned(xs, elem_bytes) || !aligned(x_scales, 4) || !aligned(xs_scales, 4))
         return FP8_ERR_ALIGN;
-    const GatherPlane rows{x, xs, H * elem_bytes, ldx * elem_bytes, elem_bytes};
-    const GatherPlane scales{x_scales, xs_scales, G * 4, ldx_scales * 4, 4};
+    const GatherPlane rows{x, xs, H * elem_bytes, ldx * elem_bytes};
+    const GatherPlane scales{x_scales, xs_scales, G * 4, ldx_scales * 4};
     clear_last_error();
     return from_hip(launch_moe_dispatch(rows, x_scales ? &scales : nullptr, slot_row, T, top_k, R,
                                         as_stream(hip_stream)));
@@ -265,7 +265,7 @@ fp8_status fp8_moe_sort_dispatch(const void *x, int elem_bytes, int64_t ldx, int
     clear_last_error();
     if (!rows) return from_hip(launch_moe_sort(r, as_stream(hip_stream)));
     return from_hip(launch_moe_sort_dispatch(
-        r, GatherPlane{x, xs, H * elem_bytes, ldx * elem_bytes, elem_bytes},
+        r, GatherPlane{x, xs, H * elem_bytes, ldx * elem_bytes},
         as_stream(hip_stream)));
 }
 

@@ -27,7 +27,6 @@ struct GatherPlane {
     const void *src;
     void *dst;
     int64_t bytes, ld;
-    int elem;  // bytes of an element: what the addresses are aligned to
 };
 hipError_t launch_moe_dispatch(const GatherPlane &rows, const GatherPlane *scales,
                                const int32_t *slot_row, int64_t T, int64_t k, int64_t R,
