@@ -337,14 +337,15 @@ def fp8_moe_sort(expert_ids, num_experts, group_offsets=None, slot_row=None, row
     return plan
 
 
-def _slots(slot_row, tokens):
+def _slots(slot_row, tokens=None):
+    """(T, k) of a plan, whose T is `tokens` unless the plan itself says it."""
     _tensor(slot_row, "slot_row", _INT)
-    if slot_row.dim() != 2 or slot_row.shape[0] != tokens:
-        raise ValueError(f"slot_row must have shape ({tokens}, top_k), got "
-                         f"{tuple(slot_row.shape)}")
+    if slot_row.dim() != 2 or tokens not in (None, slot_row.shape[0]):
+        raise ValueError(f"slot_row must have shape ({'T' if tokens is None else tokens}, top_k), "
+                         f"got {tuple(slot_row.shape)}")
     if not slot_row.is_contiguous():
         raise ValueError("slot_row must be contiguous")
-    return slot_row.shape[1]
+    return slot_row.shape
 
 
 def _row_matrix(t, name, width, dtypes):
@@ -366,7 +367,7 @@ def fp8_moe_dispatch(x, slot_row, scales=None, xs=None, xs_scales=None, stream=N
     unless given; rows that no slot names are left as they are."""
     ldx = _rows(x, "x", _COPIED)
     T, H = x.shape
-    k = _slots(slot_row, T)
+    _, k = _slots(slot_row, T)
     if xs is not None:
         _row_matrix(xs, "xs", H, (x.dtype,))
     rows = T * k if xs is None else xs.shape[0]
@@ -395,7 +396,7 @@ def fp8_moe_dispatch(x, slot_row, scales=None, xs=None, xs_scales=None, stream=N
 def _dispatch_quant(name, x, slot_row, q, scales, stream):
     ldx = _rows(x, "x", _BF16)
     T, H = x.shape
-    k = _slots(slot_row, T)
+    _, k = _slots(slot_row, T)
     G = (H + 127) // 128
     if q is not None:
         _row_matrix(q, "q", H, _U8)
@@ -504,9 +505,7 @@ def fp8_moe_dispatch_grad(dxs, slot_row, dx=None, out_dtype=None, stream=None):
     dxs [R][H] bf16 or fp32 -> dx [T][H] of out_dtype (dxs's own unless
     given)."""
     ld = _rows(dxs, "dxs", _WIDE)
-    _tensor(slot_row, "slot_row", _INT)
-    T = slot_row.shape[0]
-    k = _slots(slot_row, T)
+    T, k = _slots(slot_row)
     R, H = dxs.shape
     dtype = _dtype(out_dtype) if out_dtype is not None else dx.dtype if isinstance(
         dx, torch.Tensor) else dxs.dtype
@@ -529,9 +528,7 @@ def fp8_moe_combine(ys, slot_row, weights=None, residual=None, out=None, out_dty
     out [T][H] of out_dtype (ys's own unless given; residual may be out
     itself)."""
     ld = _rows(ys, "ys", _WIDE)
-    _tensor(slot_row, "slot_row", _INT)
-    T = slot_row.shape[0]
-    k = _slots(slot_row, T)
+    T, k = _slots(slot_row)
     R, H = ys.shape
     dtype = _dtype(out_dtype) if out_dtype is not None else out.dtype if isinstance(
         out, torch.Tensor) else ys.dtype
@@ -564,7 +561,7 @@ def fp8_moe_combine_grad(dout, ys, slot_row, weights=None, dys=None, dweights=No
     [T][k])."""
     ld_dout = _rows(dout, "dout", _WIDE)
     T, H = dout.shape
-    k = _slots(slot_row, T)
+    _, k = _slots(slot_row, T)
     ld_ys = _rows(ys, "ys", (dout.dtype,))
     R = ys.shape[0]
     if ys.shape[1] != H:
