@@ -24,13 +24,16 @@ namespace {
 // of its waves an eighth of them.  It counts its slots per wave and expert in
 // LDS; with the counts of the runs before it (several workgroups: written to
 // the workspace by a first launch) and an exclusive prefix sum over the
-// experts, every (wave, expert) has its first row.  A wave then takes its
+// experts, every (wave, expert) has its first row.  (Every workgroup adds the
+// counts of all runs: 16 runs of 32768 slots are nothing, 512 runs over 256
+// experts, a million slots, take most of the 48 us of their places.)  A wave
+// then takes its
 // slots 64 at a time in order: the lanes that hold the same expert find each
 // other by one ballot per bit of the expert's number, a lane's rank among
 // them is the population count below it.  Order is by construction, so the
 // sort is stable and the same in every run.  Latency bounds it: 32768 slots
-// over 32 experts take 4.8 us for the counts and 6.9 us for the places, up to
-// 4096 slots 4 to 8 us in one launch.
+// over 32 experts take 5 us for the counts and 7 us for the places, up to 4096
+// slots 4 to 8 us in one launch.
 constexpr int kSortWaves = 8;
 constexpr int kSortThreads = 64 * kSortWaves;
 constexpr int kSortHeld = 4;  // slots a lane holds at a time
@@ -243,12 +246,14 @@ hipError_t sort_typed(const MoeRouting &r, hipStream_t stream) {
 // are too few rows to give every thread work (kManyVecs).
 //
 // HBM bounds all of them once there are some thousand rows.  4096 tokens of
-// 7168 bf16 values, eight slots each: quantized gather 301 MB in 52 to 65 us
-// (5.8 to 4.6 TB/s, by what the caches hold of the call before); weighted sum
-// 529 MB in 97 to 106 us (5.4 to 5.0 TB/s); its gradient 998 MB in 197 us (5.1
-// TB/s); a copy of 4 GiB runs at 4.8 TB/s.  For 256 tokens the weighted sum
-// takes 8 us, for one token 3.3 us, the time of a launch that waits for two
-// loads in a row.
+// 7168 bf16 values, eight slots each, not in the caches: quantized gather 301
+// MB in 65 us (4.6 TB/s); gather of E4M3 rows 273 MB with their scales in 50 us;
+// weighted sum 529 MB in 96 to 107 us (5.5 to 4.9 TB/s); its gradient 998 MB in
+// 201 us (5.0 TB/s); a copy of 4 GiB runs at 4.8 TB/s.  For 256 tokens the
+// weighted sum takes 8 us, for one token 3.3 us, the time of a launch that waits
+// for two loads in a row.  A plane of fewer than 16 bytes a row (scales of up to
+// 384 values) goes byte by byte: 4096 x 8 rows of 384 E4M3 values 18 us with
+// scales, 5 without.
 constexpr int kRowThreads = 256;
 constexpr int kBatch = 8;
 constexpr int64_t kMaxBlocks = (int64_t)1 << 22;
@@ -450,8 +455,9 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(GatherArgs a, Row
 // all ids in L2, so there is no launch between the sort and the gather and
 // nothing to wait for.  One more row of workgroups writes the offsets.  Worth
 // it as long as the ids read in all stay few: 256 tokens of 7168 values to 8
-// experts (2 million ids) 9.5 us against 12 in two launches; 512 tokens (8
-// million) 18 us in them against 26, as measured with one id a lane at a time.
+// experts (2 million ids) 9.2 us against 11.6 in two launches (with the sort's),
+// 512 of 2048 values 7.8 against 12.5; the crossing is near 512 tokens of 7168
+// (8 million), 16.5 against 17.5.
 constexpr int64_t kFewSlots = 4096, kFewReads = (int64_t)1 << 22;
 // Ids a lane reads at a time (256 tokens: 10.9 us with one, 9.5 with four; 512
 // tokens of 2048 values 11.4 and 8.2).
@@ -825,9 +831,10 @@ namespace {
 
 // Whether the kept rows are loaded as read once, without a place in the
 // caches: from 96 MiB on, more than the caches keep until the next reader
-// (weighted sum of 8 rows of 7168 bf16 values for 4096 tokens, rows just
-// written: 227 us with the write, against 260; cold 97 against 109; gradient
-// for 2048 tokens 85 against 103; at 59 MB the other way, 13.8 against 12.3).
+// (8 rows of 7168 bf16 values a token; weighted sum for 4096 tokens: rows just
+// written 160 us with the write, against 198; not in the caches 96 against 108;
+// gradient for 2048 tokens 99 against 105; weighted sum for 512 tokens, 59 MB,
+// just written 28 with the write both ways).
 bool read_once(int64_t rows, int64_t row_bytes) { return rows * row_bytes >= 96 << 20; }
 
 }  // namespace

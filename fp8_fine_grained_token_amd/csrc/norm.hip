@@ -8,15 +8,18 @@
 //             dw1 = sum_t du yh,  dw2 = sum_t dn rh,  dg = b sum_t D yh w1
 //
 // About 14 flops a value forward and 30 backward against 7 to 18 bytes: the
-// bound is HBM.  A row stays in the registers of the threads that share it,
-// so each tensor is read and written once; a workgroup keeps the parameters
-// of its columns in registers over its rows and has the next row's loads
-// under way while a row's sums are waited for.  The statistics are FP32 sums.
-// 4096 rows of 7168 bf16 values: forward with FP8 result 206 MB in 50 us (4.1
-// TB/s; the two sums a row in series, not HBM, keep it from the 43 us of a
-// copy), gradient 352 MB in 70 to 85 us with the 5 us for the parameters' sums
-// (5.0 to 4.1 TB/s, by what the caches hold of the call before).  One row forward: 6 us, a launch and the chain of load,
-// sum, sum, store.
+// bound is HBM.  A row stays in the registers of the threads that share it, so
+// each tensor is read and written once (rows wider than kHeldForward and
+// kHeldGrad are read again: forward y three times and r twice, gradient
+// everything twice); a workgroup keeps the parameters of its columns over its
+// rows, in registers for rows of up to 512 values and in LDS for the others,
+// and has the next row's loads under way while a row's sums are waited for.
+// The statistics are FP32 sums.
+// 4096 rows of 7168 bf16 values that are not in the caches: forward with FP8
+// result 206 MB in 50 us (4.1 TB/s; the two sums a row in series, not HBM, keep
+// it from the 43 us of a copy), gradient 352 MB in 78 us and 5 us for the
+// parameters' sums.  One row forward: 6 us, a launch and the chain of load, sum,
+// sum, store.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -687,12 +690,12 @@ void with_types(const NormArgs &a, F f) {
 }
 
 // Members that share the rows: enough workgroups to keep the card's loads
-// going, as few partial rows as that allows.  One workgroup a CU is enough for
-// wide rows (4096 rows of 7168 values: 74 us, with two 79, with a half 101;
-// 1024 rows 26 and 34); shorter ones take two or four where there are rows
-// enough for each (8192 rows of 2048 values: 57 us with one, 44 with two; of
-// 1024 values 52, 35 and 27 with four; but 1024 rows of 2048 16.0 with one,
-// 17.2 with two).
+// going, as few partial rows as that allows.  Times with the reduction, inputs
+// not in the caches.  One workgroup a CU is enough for wide rows (4096 rows of
+// 7168 values: 83 us, with two 86, with a half 95; 1024 rows 28, 36 and 32);
+// shorter ones take two or four where there are rows enough for each (8192 rows
+// of 2048 values: 57 us with one, 47 with two, 48 with four; of 1024 values 53,
+// 40 and 32, with eight 38; but 1024 rows of 2048 16.1 with one, 17.6 with two).
 int64_t grad_members(int64_t T, int64_t H) {
     const RowSplit s = row_split(H);
     if (s.small) return 512 * (kSmallThreads / s.tx);

@@ -3,7 +3,10 @@
 //
 // A product of M <= 16 rows reads N K / 2 bytes of codes and N K / 32 bytes
 // of scales and does at most 64 flops per byte of them: its floor is the
-// weights' bytes at the rate of a large copy.
+// weights' bytes at the rate of a large copy.  More rows (of one expert) take a
+// pass over its weights for each 16, most of them from HBM again: 64 rows by
+// 7168 x 7168 read 42 MB for 29 and take 43 us (16 rows 13), 512 rows over 32
+// experts of 4096 x 7168 847 MB for 511 and 227 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -18,6 +21,9 @@ namespace fp8blk {
 namespace {
 
 // ---- quantizer (offline) ---------------------------------------------------
+//
+// Run once for a model's weights: 2-byte loads and 1-byte stores a lane, 4096 x
+// 7168 in 64 us (fp32 scales) and 56 us (E8M0), 1.2 and 1.3 TB/s.
 
 // E2M1 code of |y| <= 6 (ties to the even code), without the sign.
 __device__ __forceinline__ uint32_t e2m1_code(float y) {
@@ -101,8 +107,9 @@ __global__ __launch_bounds__(256) void w4_quant_kernel(const uint16_t *__restric
 // line of its own and the 64 look-ups of a load, not HBM, were the bound (128
 // rows over 32 experts of 4096 x 7168, 26 of them with rows: 131 us).  The next
 // tile's loads are under way while a tile is multiplied.  That case takes 93 to
-// 98 us (405 MB of codes and scales, 4.1 to 4.3 TB/s); one row with 2048 x 7168
-// 6.3 us, most of it the launch and one trip to HBM.
+// 100 us (405 MB of codes and scales, 4.0 to 4.3 TB/s); one row with 18432 x 7168
+// 19 us (70 MB, 3.7 TB/s), with 2048 x 7168 6.4 us, most of it the launch and
+// one trip to HBM.
 //
 // Few rows leave matrix columns unused, so kSegs of 1, 2 or 4 puts as many
 // stretches of K side by side: the 16 operand rows are then 16 / kSegs rows
@@ -506,8 +513,17 @@ __global__ __launch_bounds__(256) void w4_few_codes_kernel(
     }
 }
 
-// The kernel for `segs` stretches side by side of `per` blocks each (rounded
-// up to one that is built; the blocks too many are read twice, times zero).
+// The kernel for `segs` stretches side by side of `per` blocks each, rounded
+// up to one that is built.  What the rounding (of K to the stretches, and to a
+// build) leaves over are blocks past the row's end: the next rows' codes, read
+// and multiplied by zeros, 1.0 to 2 times the row's own.  Of short rows the
+// caches hold most of them (7168 in two stretches a wave: 8.2 MB from HBM for
+// 7.8).  6 and 7 are built because 8 in their place costs what it reads more:
+// one row by 18432 x 7168 19 us with 7, 22 with 8; by 18432 x 6144 16 with 6, 22
+// with 8; 128 rows over 32 experts of 4096 x 7168 76 and 90.  3 and 5 are not
+// built: those rows take 4 and 6.  Rows of more than 64 blocks (K past 8192) go
+// in chunks of 64 and spill: one row by 7168 x 18432 (144 blocks, 192 read)
+// takes 46 us, 121 MB from HBM for 70 and 31 MB of spills written.
 using MatvecKernel = void (*)(const Bf16 *, const uint8_t *, const uint8_t *, const int32_t *,
                               W4Shape, void *);
 template <bool kE8m0>
@@ -566,7 +582,7 @@ hipError_t launch_w4_matvec(const void *x, int64_t ldx, const void *codes, const
     // Workgroups that can be busy: experts with rows times column tiles.
     // Stretches of K side by side (kSegs) and waves along K (split) both make
     // more and narrower tiles; they are taken as far as the card needs them
-    // (one row: 2048 x 7168 8.0 us without, 6.5 with; 1037 x 1000 9.6 and 4.3).
+    // (one row: 2048 x 7168 8.2 us without, 6.6 with; 1037 x 1000 8.8 and 4.0).
     const int64_t active = offsets ? (E < R ? E : R) : 1;
     const int64_t want = 256;
     int segs = 1, split_log = 0;
@@ -591,10 +607,10 @@ hipError_t launch_w4_matvec(const void *x, int64_t ldx, const void *codes, const
     p.steps = 1;
     // Column tiles of a wave: x is read once for all of them and the next
     // tile's loads overlap the products, so dense grids stay at one workgroup a
-    // CU (16 rows by 18432 x 7168: 21 us, with 1024 workgroups 32).  Experts
-    // differ in their rows and some have none, so theirs are dealt in smaller
-    // pieces (128 rows over 32 experts of 4096 x 7168: 104 us with 1024, 153
-    // with 256 or 4096).
+    // CU (16 rows by 18432 x 7168: 21 us, with 512 workgroups 27, with 1024 32).
+    // Experts differ in their rows and some have none, so theirs are dealt in
+    // smaller pieces (128 rows over 32 experts of 4096 x 7168, 22 of them with
+    // rows: 76 us with 1024 workgroups, with 512 122, with 2048 89).
     const int64_t target = offsets ? 1024 : 256;
     if (total * active > target) p.steps = (int)((total * active + target - 1) / target);
     const dim3 grid((unsigned)((total + p.steps - 1) / p.steps), (unsigned)active);

@@ -11,6 +11,9 @@
   * 4-bit weights: ``fp8_w4_quant_1x128``, ``fp8_w4_quant_1x32``,
     ``fp8_w4_matvec``, ``fp8_w4_grouped_matvec``.
 
+Results carry no autograd graph, whatever the inputs' ``requires_grad``: the
+gradients are the ``_grad`` calls.
+
 As in ``binding``: argument marshalling only, outputs and workspaces are
 allocated when not given, and shapes are checked before anything is launched,
 because the kernels index every buffer by the sizes they are given; outputs

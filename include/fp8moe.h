@@ -20,7 +20,8 @@
  *     group that holds one is quantized so that it reads back as NaN: its
  *     scale is the largest magnitude (NaN, else infinity), with power-of-two
  *     scales too, and its codes are NaN.
- *   - Sums, norms and products are FP32; an output is rounded once, to
+ *   - Sums, norms and products are FP32 (the squares of a norm too: values
+ *     from about 1e19 on are past their range); an output is rounded once, to
  *     nearest even.  Results do not depend on the run: no sum uses
  *     floating-point atomics.
  *   - Sizes of zero are valid; nothing is written but what a sum over nothing
@@ -198,8 +199,9 @@ fp8_status fp8_norm_residual_quant_1x128_pow2(
  * dn, y and dy have y_dtype; dr_out, r_out and dr have r_dtype.  y, r_out,
  * rstd_post and rstd_pre are the forward's (rstd_post is not read where
  * post_norm is 0; r_out and rstd_pre are not read where dn is NULL).
- *   workspace  fp8_norm_residual_grad_workspace_bytes() bytes, 16-byte
- *              aligned (NULL where that is 0)
+ *   workspace  fp8_norm_residual_grad_workspace_bytes() bytes (asked for with
+ *              gate_rows 1 where there is no gate), 16-byte aligned (NULL
+ *              where that is 0)
  * With T = 0 the fp32 gradients are zeros.
  */
 fp8_status fp8_norm_residual_grad(const void *dn, int64_t ld_dn, const void *dr_out,
