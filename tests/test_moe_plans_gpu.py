@@ -369,3 +369,20 @@ def test_gradients_of_many_rows(T, H, y_type, r_type, gates, post):
     got = M.fp8_norm_residual_grad(c.dn, c.dr_out, c.y, r_out, rs1, rs2, c.w_post, c.gate, c.w_pre,
                                    **c.kw)
     c.check_gradient(r_out, rs1, rs2, got)
+
+
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("H", [5, 40, 1500, 4001, 9000])
+def test_gradient_left_out_is_zero(H, post):
+    t = torch()
+    c = Norms(24, H, "bf16", "f32", 3, post, seed=20)
+    r_out, _, rs1, rs2 = M.fp8_norm_residual(*c.args(), eps=c.eps, **c.kw)
+
+    def grad(dn, dr_out, rs2):
+        return M.fp8_norm_residual_grad(dn, dr_out, c.y, r_out, rs1, rs2, c.w_post, c.gate,
+                                        c.w_pre, **c.kw)
+
+    for got, want in ((grad(None, c.dr_out, None), grad(t.zeros_like(c.dn), c.dr_out, rs2)),
+                      (grad(c.dn, None, rs2), grad(c.dn, t.zeros_like(c.dr_out), rs2))):
+        for a, b in zip(got, want):
+            assert (a is None and b is None) or t.equal(a, b)
