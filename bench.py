@@ -61,7 +61,8 @@ PEAK_FP8_TFLOPS = 5000.0   # MI355X dense FP8 MFMA
 MAX_SCLK_MHZ = 2400.0      # the clock that peak is quoted at
 PEAK_HBM_GBS = 8000.0      # MI355X HBM3E
 COUNTERS_FILE = os.path.join(ROOT, "profiles", "counters_dense_gemm.json")
-GEMM_SOURCE = os.path.join(ROOT, "fp8_fine_grained_token_amd", "csrc", "gemm.hip")
+GEMM_SOURCES = [os.path.join(ROOT, "fp8_fine_grained_token_amd", "csrc", name)
+                for name in ("gemm.hip", "gemm_tile.hpp")]
 
 M, N, K = 4096, 7168, 7168
 CPU_SAMPLE_ROWS = 512   # ~11 s of oracle work on 16 host threads
@@ -74,13 +75,15 @@ def log(msg):
     print(msg, file=sys.stderr, flush=True)
 
 
-def code_hash(path):
-    """sha256 of a C/C++/HIP source with its comments removed and its blank
+def code_hash(paths):
+    """sha256 of C/C++/HIP sources with their comments removed and their blank
     space collapsed: it changes when the code changes, not when only its
     comments do."""
     import re
-    with open(path, encoding="utf-8") as f:
-        text = f.read()
+    text = ""
+    for path in paths:
+        with open(path, encoding="utf-8") as f:
+            text += f.read() + "\n"
     text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
     text = re.sub(r"//[^\n]*", " ", text)
     return hashlib.sha256(" ".join(text.split()).encode()).hexdigest()
@@ -96,13 +99,13 @@ def quant_bytes(m, k):
 
 def traffic_from_counters():
     """HBM bytes per GEMM launch from the committed counter summary, or None
-    when it is missing or was taken on different gemm.hip code."""
+    when it is missing or was taken on different GEMM code."""
     try:
         with open(COUNTERS_FILE) as f:
             c = json.load(f)
     except (OSError, ValueError):
         return None
-    if c.get("gemm_code_sha256") != code_hash(GEMM_SOURCE):
+    if c.get("gemm_code_sha256") != code_hash(GEMM_SOURCES):
         return None
     return c.get("hbm_bytes_per_launch")
 

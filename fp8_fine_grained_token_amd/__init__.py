@@ -28,17 +28,31 @@ _MOE = (
     "fp8_w4_matvec", "fp8_w4_grouped_matvec",
 )
 
+_FFN = (
+    "FP8_ACT_SILU", "FP8_ACT_GELU_TANH", "fp8_block_gemm_gated", "fp8_block_gemm_gated_pow2",
+    "fp8_block_gemm_gated_quant_1x128", "fp8_block_gemm_gated_quant_1x128_pow2",
+    "fp8_gated_gemm_workspace_bytes", "fp8_grouped_gated_gemm_workspace_bytes",
+    "fp8_block_grouped_gemm_gated",
+    "fp8_block_grouped_gemm_gated_pow2", "fp8_block_grouped_gemm_gated_quant_1x128",
+    "fp8_block_grouped_gemm_gated_quant_1x128_pow2", "fp8_gated_grad",
+    "fp8_gated_grad_quant_1x128", "fp8_gated_grad_quant_1x128_pow2", "fp8_gated_grad_quant",
+    "fp8_gated_grad_quant_pow2", "fp8_dequant_act_1x128", "fp8_requant_act_128x1_t",
+    "fp8_requant_act_128x1_t_pow2", "fp8_block_grouped_gemm_dgrad",
+    "fp8_block_grouped_gemm_dgrad_pow2",
+)
+
 
 def __getattr__(name):
-    """The operators around the expert products, from ``moe`` on first use
-    (it needs torch, which importing this package does not load)."""
-    if name in _MOE:
-        from . import moe
-        value = getattr(moe, name)
+    """The operators around the expert products, from ``moe``, and inside a
+    gated feed-forward block, from ``ffn``, on first use (they need torch, which
+    importing this package does not load)."""
+    if name in _MOE or name in _FFN:
+        from . import ffn, moe
+        value = getattr(moe if name in _MOE else ffn, name)
         globals()[name] = value
         return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def __dir__():
-    return sorted(set(globals()) | set(_MOE))
+    return sorted(set(globals()) | set(_MOE) | set(_FFN))

@@ -1,0 +1,480 @@
+// Gated products: both projections of a gated feed-forward block, the
+// activation and their product in one kernel,
+//   g = x Wg^T, u = x Wu^T, a = act(g) u,
+// from E4M3 operands with 1x128 and 128x128 scales (W [2 I][K], the gate's
+// rows first), dense or per expert.
+//
+// The tile is the block GEMM's (gemm_tile.hpp) with 128 columns of the gate
+// and the same 128 columns of the other projection side by side, so that a
+// workgroup holds both factors of its 128 columns of a.  128 columns are also
+// one 1x128 scale group of a, of g and of u: each is quantized where it is
+// made, and neither g, u nor a passes through memory in 16 bits.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.hpp"
+#include "gated.hpp"
+#include "gemm_tile.hpp"
+#include "launch_ffn.hpp"
+
+namespace fp8blk {
+
+namespace {
+
+constexpr int kCUs = 256;
+
+// Fused tiles: 256 x 256 and 128 x 256 (BigTile, MidTile), and 32 x 256 for few
+// rows to a matrix of weights.
+using RowTile = TileCfg<32, 256, 1, 4, 4>;
+// Tiles of a part of the projections (plain products with 2 I columns).
+using PartTile = TileCfg<64, 64, 2, 2, 4>;
+using RowPartTile = TileCfg<32, 64, 1, 4, 4>;
+
+struct GatedParams {
+    const uint8_t *a;
+    const float *sa;
+    const uint8_t *w;
+    const float *sw;
+    const int32_t *offsets;
+    int64_t M, I, K;
+    int G, E;
+    int tiles_m, tiles_n, ntiles, group_m;
+    GatedOut to;
+    // split plan: K blocks of a part, parts, their sums [ksplit][M][2 I]
+    int kb_per_split, ksplit;
+    float *partial;
+};
+
+// Writes a tile from its accumulators: the tile goes through the free LDS
+// stages in FP32 (laid out as in tile_store_buf: the 32-byte piece q of row r
+// at piece q ^ (r % 16)), as many rows at a time as fit, and comes back as
+// rows, 16 lanes to a row and 8 columns of both halves to a lane.
+template <class C>
+__device__ __forceinline__ void gated_store(const v4f (&acc)[C::kTM][C::kTN], TileLds<C> &L,
+                                            const GatedOut &to, int64_t row0, int64_t row_end,
+                                            int64_t n0) {
+    static_assert(C::BN == 256, "128 columns of either half");
+    constexpr int kRB = C::BN * 4;
+    constexpr int kFit = (int)(sizeof(L.stages) / kRB) / C::WM * C::WM;
+    constexpr int kRowsPerPass = kFit < C::BM ? kFit : C::BM;
+    static_assert(kRowsPerPass >= C::WM && C::BM % kRowsPerPass == 0, "store passes");
+    static_assert(kRowsPerPass % (C::kThreads / 16) == 0, "whole waves");
+    uint8_t *buf = reinterpret_cast<uint8_t *>(&L.stages[0]);
+    auto piece = [&](int r, int q) { return buf + r * kRB + ((q ^ (r & 15)) << 5); };
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = tid >> 6;
+    const int wn = wave % C::kWavesN;
+    const int wave_row0 = __builtin_amdgcn_readfirstlane(wave / C::kWavesN * C::WM);
+#pragma unroll
+    for (int r_lo = 0; r_lo < C::BM; r_lo += kRowsPerPass) {
+        __syncthreads();  // the stages (or the previous pass) are no longer read
+        if (wave_row0 >= r_lo && wave_row0 < r_lo + kRowsPerPass) {
+#pragma unroll
+            for (int i = 0; i < C::kTM; ++i) {
+                const int r = wave_row0 - r_lo + 16 * i + (lane & 15);
+#pragma unroll
+                for (int j = 0; j < C::kTN; ++j) {
+                    const int cb = (wn * C::WN + 16 * j + 4 * (lane >> 4)) * 4;
+                    *reinterpret_cast<v4f *>(piece(r, cb >> 5) + (cb & 31)) = acc[i][j];
+                }
+            }
+        }
+        __syncthreads();
+        for (int r = tid >> 4; r < kRowsPerPass; r += C::kThreads / 16) {
+            const int64_t row = row0 + r_lo + r;
+            float g[8], u[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const v4f x = *reinterpret_cast<const v4f *>(piece(r, tid & 15) + 16 * h);
+                const v4f y = *reinterpret_cast<const v4f *>(piece(r, 16 + (tid & 15)) + 16 * h);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    g[4 * h + i] = x[i];
+                    u[4 * h + i] = y[i];
+                }
+            }
+            put_gated(to, row, n0, row < row_end, g, u);
+        }
+    }
+}
+
+// kExact: products on the bf16 MFMA (gemm_tile.hpp), any scales.
+template <class C, bool kPow2, bool kExact>
+__device__ __forceinline__ void gated_tile(const GatedParams &p, TileLds<C> &lds, const uint8_t *w,
+                                           const float *sw, int64_t row0, int64_t row_end,
+                                           int64_t n0) {
+    v4f acc[C::kTM][C::kTN];
+    const TwoPartOperands op =
+        tile_operands_gated<C>(p.a, p.sa, w, sw, row0, row_end - row0, n0, p.I, p.K, p.G);
+    const int wn = (threadIdx.x >> 6) % C::kWavesN;
+    tile_mainloop<C, kPow2, false, TwoPartOperands, kExact>(op, p.K, p.G, 0, p.G, wn * C::WN, lds,
+                                                            acc);
+    gated_store<C>(acc, lds, p.to, row0, row_end, n0);
+}
+
+template <class C, bool kPow2>
+__global__ __launch_bounds__(C::kThreads) void gated_gemm_kernel(GatedParams p) {
+    __shared__ TileLds<C> lds;
+    const int t = xcd_logical_tile();
+    if (t >= p.ntiles) return;
+    int tm, tn;
+    raster(t, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+    gated_tile<C, kPow2, false>(p, lds, p.w, p.sw, (int64_t)tm * C::BM, p.M, (int64_t)tn * 128);
+}
+
+template <class C, bool kPow2, bool kExact>
+__global__ __launch_bounds__(C::kThreads) void gated_grouped_kernel(GatedParams p) {
+    __shared__ TileLds<C> lds;
+    __shared__ int64_t info[4];
+    find_grouped_tile<C::BM>(p.offsets, p.E, (int)p.M, p.tiles_n, info);
+    const int64_t e = info[0];
+    if (e < 0) return;
+    gated_tile<C, kPow2, kExact>(p, lds, p.w + e * 2 * p.I * p.K, p.sw + e * 2 * (p.I >> 7) * p.G,
+                                 info[1], info[2], info[3] * 128);
+}
+
+// ---- few tiles: parts of the projections, then their sums ----
+
+// [g | u] of one part of K: a plain product with 2 I columns.  These are the
+// calls whose time goes into latency and weight bytes, so the products run on
+// the bf16 MFMA, whose sums are FP32.
+template <class C, bool kGrouped>
+__global__ __launch_bounds__(C::kThreads) void gated_partial_kernel(GatedParams p) {
+    __shared__ TileLds<C> lds;
+    __shared__ int64_t info[4];
+    const uint8_t *w = p.w;
+    const float *sw = p.sw;
+    int64_t row0, row_end;
+    int tn, ks;
+    if constexpr (kGrouped) {
+        find_grouped_tile<C::BM>(p.offsets, p.E, (int)p.M, p.tiles_n * p.ksplit, info);
+        const int64_t e = info[0];
+        if (e < 0) return;
+        w += e * 2 * p.I * p.K;
+        sw += e * 2 * (p.I >> 7) * p.G;
+        row0 = info[1];
+        row_end = info[2];
+        ks = (int)info[3] / p.tiles_n;
+        tn = (int)info[3] - ks * p.tiles_n;
+    } else {
+        const int t = xcd_logical_tile();
+        if (t >= p.ntiles) return;
+        const int per_split = p.tiles_m * p.tiles_n;
+        ks = t / per_split;
+        int tm;
+        raster(t - ks * per_split, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+        row0 = (int64_t)tm * C::BM;
+        row_end = p.M;
+    }
+    const int64_t n0 = (int64_t)tn * C::BN, N = 2 * p.I;
+    const int kb0 = ks * p.kb_per_split, kb1 = min(kb0 + p.kb_per_split, p.G);
+    v4f acc[C::kTM][C::kTN];
+    const TileOperands op =
+        tile_operands<C>(p.a, p.sa, w, sw, row0, row_end - row0, n0, N - n0, p.K, p.G);
+    const int wn = (threadIdx.x >> 6) % C::kWavesN;
+    tile_mainloop<C, false, false, TileOperands, true>(op, p.K, p.G, kb0, kb1,
+                                                       (int)(n0 & 127) + wn * C::WN, lds, acc);
+    tile_store<C, kOutF32>(acc, lds, p.partial + (int64_t)ks * p.M * N, N, row0, row_end, n0, N);
+}
+
+// ---- very few rows: the weights straight to registers ----
+
+// A workgroup makes 8 columns of the gate and the same 8 of the other
+// projection, the 16 rows of W of a matrix instruction, for up to 16 rows of x
+// (which are its columns).  Its 16 waves take K blocks in turn and add up in LDS
+// in their order, so a workgroup has its columns' whole sums (or, with K split
+// over workgroups too, its part's).  All loads of a wave's next four blocks are
+// under way at once: with 256 workgroups that is every byte of 2 x 2048 x 7168
+// weights.  Four lanes read a row's 128 bytes of a block, in two halves.
+constexpr int kFewRows = 16, kFewWaves = 16, kFewBatch = 4;
+
+__device__ __forceinline__ v8i two_halves(const u32x4 &lo, const u32x4 &hi) {
+    v8i f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        f[k] = (int)lo[k];
+        f[4 + k] = (int)hi[k];
+    }
+    return f;
+}
+
+__global__ __launch_bounds__(64 * kFewWaves) void gated_few_kernel(GatedParams p) {
+    __shared__ float lds[kFewWaves][kFewRows][16];
+    const int t = xcd_logical_tile();
+    if (t >= p.ntiles) return;
+    const int ks = t / p.tiles_n, tn = t - ks * p.tiles_n;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane & 15, q = lane >> 4;
+    const int rows = (int)p.M;
+    const int64_t n0 = 8 * (int64_t)tn;
+    // W row r: the gate's n0 + r, or the other's n0 + r - 8
+    const uint8_t *wp = p.w + ((r < 8 ? 0 : p.I - 8) + n0 + r) * p.K + 16 * q;
+    // this lane's outputs are W rows 4 q .. 4 q + 3: one half, one scale block
+    const float *swp = p.sw + ((q < 2 ? 0 : p.I >> 7) + (n0 >> 7)) * p.G;
+    const int64_t m = min(r, rows - 1);  // past the last row: it again
+    const uint8_t *xp = p.a + m * p.K + 16 * q;
+    const float *sap = p.sa + m * p.G;
+    const int kb0 = ks * p.kb_per_split, kb1 = min(kb0 + p.kb_per_split, p.G);
+    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int base = kb0 + wave; base < kb1; base += kFewWaves * kFewBatch) {
+        v8i wv[kFewBatch], xv[kFewBatch];
+        float sw[kFewBatch], sa[kFewBatch];
+#pragma unroll
+        for (int b = 0; b < kFewBatch; ++b) {
+            const int64_t kb = base + kFewWaves * b;
+            if (kb < kb1) {
+                const u32x4 *w = reinterpret_cast<const u32x4 *>(wp + kb * 128);
+                const u32x4 *x = reinterpret_cast<const u32x4 *>(xp + kb * 128);
+                wv[b] = two_halves(__builtin_nontemporal_load(w),
+                                   __builtin_nontemporal_load(w + 4));
+                xv[b] = two_halves(x[0], x[4]);
+                sw[b] = swp[kb];
+                sa[b] = sap[kb];
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < kFewBatch; ++b) {
+            if (base + kFewWaves * b < kb1) {
+                v8bf wb[4], xb[4];
+                to_bf16(wv[b], wb);
+                to_bf16(xv[b], xb);
+                const v4f c = mfma_bf16(wb, xb);
+                const float f = sa[b] * sw[b];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(c[e], f, acc[e]);
+            }
+        }
+    }
+    *reinterpret_cast<v4f *>(&lds[wave][r][4 * q]) = acc;
+    __syncthreads();
+    // one thread to a row's column of a: the sums of g and of u
+    const int row = threadIdx.x >> 3, c = threadIdx.x & 7;
+    if (row >= rows) return;
+    float g = 0.0f, u = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kFewWaves; ++k) {
+        g += lds[k][row][c];
+        u += lds[k][row][8 + c];
+    }
+    if (p.partial) {
+        float *d = p.partial + ((int64_t)ks * p.M + row) * 2 * p.I + n0 + c;
+        d[0] = g;
+        d[p.I] = u;
+    } else {
+        const float s = p.to.gelu ? gate_sigmoid<true>(g) : gate_sigmoid<false>(g);
+        const float v = g * s * u;
+        const int64_t at = row * p.I + n0 + c;
+        if (p.to.bf16_out)
+            from_float(v, static_cast<Bf16 *>(p.to.out)[at]);
+        else
+            static_cast<float *>(p.to.out)[at] = v;
+    }
+}
+
+// Adds the parts in their order and writes what the call asks for, 16 lanes to
+// a row's 128 columns.  Grouped: rows of the experts' ranges only, which run
+// from the first offset to the largest (find_grouped_tile).
+template <bool kGrouped>
+__global__ __launch_bounds__(256) void gated_finish_kernel(GatedParams p) {
+    const int64_t GI = p.I >> 7;
+    const int64_t id = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    bool live = id < p.M * GI;
+    const int64_t row = live ? id / GI : 0, gb = live ? id % GI : 0;
+    if constexpr (kGrouped) {
+        const int T = (int)p.M;
+        const int first = min(max(p.offsets[0], 0), T);
+        int last = 0;
+        for (int e = threadIdx.x & 63; e <= p.E; e += 64) last = max(last, min(p.offsets[e], T));
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) last = max(last, __shfl_xor(last, d));
+        live = live && row >= first && row < last;
+    }
+    const int64_t at = row * 2 * p.I + 128 * gb + 8 * (threadIdx.x & 15);
+    float g[8] = {}, u[8] = {};
+    if (live) {
+        for (int k = 0; k < p.ksplit; ++k) {
+            const float *s = p.partial + (int64_t)k * p.M * 2 * p.I + at;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const v4f x = __builtin_nontemporal_load(reinterpret_cast<const v4f *>(s) + h);
+                const v4f y =
+                    __builtin_nontemporal_load(reinterpret_cast<const v4f *>(s + p.I) + h);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    g[4 * h + i] += x[i];
+                    u[4 * h + i] += y[i];
+                }
+            }
+        }
+    }
+    put_gated(p.to, row, 128 * gb, live, g, u);
+}
+
+inline int round_up(int x, int m) { return (x + m - 1) / m * m; }
+
+// ---- which way a product runs ----
+//
+// kFused is one kernel; the others make the projections in parts of K, whose
+// sums need a workspace, and add them up in a second one.  Figures: us on the
+// GPU, quantized result, K 7168 unless said, operands from HBM.
+//   kFew (16 rows at most, one round of workgroups): 1 row of 2 x 2048 columns
+//     11.7 (9.2 where it needs no second kernel), 16 rows 15.3, against 14.8 and
+//     15.9 for kParts; past 2^24 values of I K or 2048 columns kParts is ahead
+//     (16 rows of 2 x 4096 26 against 18).
+//   kParts: 128 rows of 2 x 1024 19 against 63 fused, 512 rows 32 against 62,
+//     1024 rows 56 against 63, 1536 rows and K 4096 51 against 41: so up to 64
+//     tiles of 128 x 256.  Few rows (32-row tiles): as long as the fused tiles
+//     leave CUs without work.
+// Few rows to a matrix of weights (32 on average at most) run on 32-row tiles
+// with bf16 products, which the weights' copies hide: 128 rows over 32 experts
+// of 2 x 2048 131 us against 148 for 128-row FP8 tiles, 512 rows 178 against
+// 215, 1024 rows 217 against 214.
+enum Way { kFused, kFew, kParts };
+struct Plan {
+    Way way;
+    int ksplit, per;  // parts of K, K blocks of a part
+};
+constexpr int64_t kFewTiles = 64;
+constexpr int64_t kFewColumns = 8 * kCUs, kFewValues = (int64_t)1 << 24;
+constexpr int64_t kRowsPerMatrix = 32;
+constexpr int64_t kPartExperts = 1024;  // the second kernel's workgroups read all offsets
+
+bool few_rows(int64_t M, int64_t E) { return M <= kRowsPerMatrix * (E ? E : 1); }
+// Row tiles of M rows over E experts (0: dense), at most: one more for every
+// expert that has rows.
+int64_t row_tiles(int64_t M, int64_t E, int rows) {
+    return (M + rows - 1) / rows + (E < M ? E : M);
+}
+
+Plan plan_gated(int64_t M, int64_t E, int64_t I, int64_t K) {
+    const int G = (int)(K / 128);
+    const bool few = few_rows(M, E);
+    int64_t tiles, most = 2 * kCUs;  // two workgroups of kParts fit a CU
+    int least = 4;                   // K blocks that a part keeps
+    Way way = kParts;
+    if (!E && M <= kFewRows && I <= kFewColumns && I * K <= kFewValues) {
+        way = kFew;
+        tiles = I / 8;
+        most = kCUs;
+        least = kFewWaves;
+    } else if (E <= kPartExperts && (few ? row_tiles(M, E, RowTile::BM) * (I / 128) < kCUs
+                                         : row_tiles(M, E, MidTile::BM) * (I / 128) <= kFewTiles)) {
+        static_assert(PartTile::BN == RowPartTile::BN, "column tiles");
+        tiles = row_tiles(M, E, few ? RowPartTile::BM : PartTile::BM) * (2 * I / PartTile::BN);
+    } else {
+        return {kFused, 1, G};
+    }
+    int s = 1;
+    while (tiles * s * 2 <= most && G / (s * 2) >= least) s *= 2;
+    const int per = (G + s - 1) / s;
+    return {way, (G + per - 1) / per, per};
+}
+
+size_t plan_bytes(const Plan &s, int64_t M, int64_t I) {
+    if (s.way == kFused) return 0;
+    return (size_t)s.ksplit * (size_t)M * (size_t)(2 * I) * sizeof(float);
+}
+
+template <class C>
+void launch_part_tiles(GatedParams &p, hipStream_t stream) {
+    p.tiles_n = (int)(2 * p.I / C::BN);
+    p.tiles_m = (int)row_tiles(p.M, p.E, C::BM);
+    p.ntiles = p.tiles_m * p.tiles_n * p.ksplit;
+    const dim3 grid(round_up(p.ntiles, kNumXcd));
+    if (p.offsets)
+        hipLaunchKernelGGL((gated_partial_kernel<C, true>), grid, dim3(C::kThreads), 0, stream, p);
+    else
+        hipLaunchKernelGGL((gated_partial_kernel<C, false>), grid, dim3(C::kThreads), 0, stream,
+                           p);
+}
+
+hipError_t launch_parts(GatedParams &p, const Plan &s, hipStream_t stream) {
+    p.ksplit = s.ksplit;
+    p.kb_per_split = s.per;
+    if (s.way == kFew) {
+        p.tiles_n = (int)(p.I / 8);
+        p.ntiles = p.tiles_n * p.ksplit;
+        // whole sums of the only output need no second kernel
+        if (s.ksplit == 1 && !p.to.q) p.partial = nullptr;
+        hipLaunchKernelGGL(gated_few_kernel, dim3(round_up(p.ntiles, kNumXcd)),
+                           dim3(64 * kFewWaves), 0, stream, p);
+        if (!p.partial) return hipGetLastError();
+    } else if (few_rows(p.M, p.E)) {
+        launch_part_tiles<RowPartTile>(p, stream);
+    } else {
+        launch_part_tiles<PartTile>(p, stream);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const dim3 finish((unsigned)((p.M * (p.I >> 7) + 15) / 16));
+    if (p.offsets)
+        hipLaunchKernelGGL(gated_finish_kernel<true>, finish, dim3(256), 0, stream, p);
+    else
+        hipLaunchKernelGGL(gated_finish_kernel<false>, finish, dim3(256), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <class C>
+hipError_t launch_dense_tiles(GatedParams &p, hipStream_t stream) {
+    p.tiles_m = (int)((p.M + C::BM - 1) / C::BM);
+    p.ntiles = p.tiles_m * p.tiles_n;
+    const dim3 grid(round_up(p.ntiles, kNumXcd));
+    if (p.to.pow2)
+        hipLaunchKernelGGL((gated_gemm_kernel<C, true>), grid, dim3(C::kThreads), 0, stream, p);
+    else
+        hipLaunchKernelGGL((gated_gemm_kernel<C, false>), grid, dim3(C::kThreads), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <class C, bool kExact>
+hipError_t launch_grouped_tiles(GatedParams &p, hipStream_t stream) {
+    p.tiles_m = (int)row_tiles(p.M, p.E, C::BM);
+    const dim3 grid(round_up(p.tiles_m * p.tiles_n, kNumXcd));
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(C::kThreads), 0, stream, p);
+        return hipGetLastError();
+    };
+    if constexpr (kExact)
+        return go(gated_grouped_kernel<C, false, true>);
+    else
+        return p.to.pow2 ? go(gated_grouped_kernel<C, true, false>)
+                         : go(gated_grouped_kernel<C, false, false>);
+}
+
+}  // namespace
+
+size_t gated_gemm_workspace_bytes(int64_t M, int64_t E, int64_t I, int64_t K) {
+    return plan_bytes(plan_gated(M, E, I, K), M, I);
+}
+
+hipError_t launch_gated_gemm(const GatedGemm &g, hipStream_t stream) {
+    GatedParams p{};
+    p.a = static_cast<const uint8_t *>(g.a);
+    p.sa = g.sa;
+    p.w = static_cast<const uint8_t *>(g.w);
+    p.sw = g.sw;
+    p.offsets = g.offsets;
+    p.M = g.M;
+    p.I = g.to.I;
+    p.K = g.K;
+    p.G = (int)(g.K / 128);
+    p.E = g.offsets ? (int)g.E : 0;
+    p.tiles_n = (int)(p.I / 128);
+    p.group_m = 8;
+    p.to = g.to;
+    const Plan s = plan_gated(p.M, p.E, p.I, p.K);
+    if (s.way != kFused && g.workspace && g.workspace_bytes >= plan_bytes(s, p.M, p.I)) {
+        p.partial = static_cast<float *>(g.workspace);
+        return launch_parts(p, s, stream);
+    }
+    if (g.offsets)
+        return few_rows(p.M, p.E) ? launch_grouped_tiles<RowTile, true>(p, stream)
+                                  : launch_grouped_tiles<MidTile, false>(p, stream);
+    const int64_t big = ((p.M + BigTile::BM - 1) / BigTile::BM) * p.tiles_n;
+    if (big >= kCUs) return launch_dense_tiles<BigTile>(p, stream);
+    return launch_dense_tiles<MidTile>(p, stream);
+}
+
+}  // namespace fp8blk

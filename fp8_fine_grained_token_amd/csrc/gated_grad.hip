@@ -1,0 +1,403 @@
+// Backward side of a gated feed-forward block: the gradient of a = act(g) u
+// from a checkpoint of [g | u] (E4M3 with 1x128 scales, or bf16),
+//   dg = da u act'(g), du = da act(g),
+// as it is or quantized for the products that follow it, and 8-bit
+// checkpoints read back or turned for a weight gradient.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.hpp"
+#include "gated.hpp"
+#include "launch_ffn.hpp"
+#include "vec.hpp"
+
+namespace fp8blk {
+
+namespace {
+
+// Four E4M3 bytes -> fp32 (exact).
+__device__ __forceinline__ void e4m3x4(uint32_t w, float (&f)[4]) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    f[0] = lo[0]; f[1] = lo[1]; f[2] = hi[0]; f[3] = hi[1];
+}
+__device__ __forceinline__ void e4m3x8(u32x2_any w, float s, float (&f)[8]) {
+    float a[4], b[4];
+    e4m3x4(w.x, a);
+    e4m3x4(w.y, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[i] = a[i] * s;
+        f[4 + i] = b[i] * s;
+    }
+}
+
+template <bool kGelu>
+__device__ __forceinline__ void grad8(const float (&g)[8], const float (&u)[8],
+                                      const float (&da)[8], float (&dg)[8], float (&du)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float a;
+        gated_grad<kGelu>(g[i], u[i], da[i], dg[i], du[i], a);
+    }
+}
+
+// g and u of one row's 8 columns as they are stored, and as fp32.
+template <bool kH8>
+struct RawH;
+template <>
+struct RawH<true> {
+    u32x2_any g, u;
+    float sg, su;
+    __device__ __forceinline__ void load(const GatedGrad &p, int64_t row, int64_t col) {
+        const uint8_t *h = static_cast<const uint8_t *>(p.h) + row * p.ld_h + col;
+        g = *reinterpret_cast<const u32x2_any *>(h);
+        u = *reinterpret_cast<const u32x2_any *>(h + p.I);
+        const int64_t GI = p.I >> 7;
+        const float *s = p.h_scales + row * 2 * GI + (col >> 7);
+        sg = s[0];
+        su = s[GI];
+    }
+    __device__ __forceinline__ void get(float (&fg)[8], float (&fu)[8]) const {
+        e4m3x8(g, sg, fg);
+        e4m3x8(u, su, fu);
+    }
+};
+template <>
+struct RawH<false> {
+    Raw8<Bf16> g, u;
+    __device__ __forceinline__ void load(const GatedGrad &p, int64_t row, int64_t col) {
+        const Bf16 *h = static_cast<const Bf16 *>(p.h) + row * p.ld_h + col;
+        load_raw<false>(h, 8, g);
+        load_raw<false>(h + p.I, 8, u);
+    }
+    __device__ __forceinline__ void get(float (&fg)[8], float (&fu)[8]) const {
+        unpack(g, fg);
+        unpack(u, fu);
+    }
+};
+
+// Row by row: 16 lanes to a row's 128 columns, 8 to a lane.
+template <class Da, bool kH8, bool kGelu>
+__global__ __launch_bounds__(256) void gated_grad_rows_kernel(GatedGrad p) {
+    const int64_t GI = p.I >> 7;
+    const int64_t id = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const bool live = id < p.M * GI;
+    const int64_t row = live ? id / GI : p.M - 1, gb = live ? id % GI : 0;
+    const int64_t col = 128 * gb + 8 * (threadIdx.x & 15);
+    Raw8<Da> da_raw;
+    RawH<kH8> h_raw;
+    load_raw<false>(static_cast<const Da *>(p.da) + row * p.ld_da + col, 8, da_raw);
+    h_raw.load(p, row, col);
+    float da[8], g[8], u[8], dg[8], du[8];
+    unpack(da_raw, da);
+    h_raw.get(g, u);
+    grad8<kGelu>(g, u, da, dg, du);
+    if (p.dh && live) {
+        const Span s{(int)col, 0, 8};
+        if (p.dh_bf16) {
+            store_span(static_cast<Bf16 *>(p.dh) + row * 2 * p.I, s, dg);
+            store_span(static_cast<Bf16 *>(p.dh) + (row * 2 + 1) * p.I, s, du);
+        } else {
+            store_span(static_cast<float *>(p.dh) + row * 2 * p.I, s, dg);
+            store_span(static_cast<float *>(p.dh) + (row * 2 + 1) * p.I, s, du);
+        }
+    }
+    if (p.q) {
+        put_quantized(dg, live, p.pow2, p.q + row * 2 * p.I + col, p.scales + row * 2 * GI + gb);
+        put_quantized(du, live, p.pow2, p.q + (row * 2 + 1) * p.I + col,
+                      p.scales + (row * 2 + 1) * GI + gb);
+    }
+}
+
+// Eight rows (tokens) m .. m + 7 of one column k, quantized over the 128 rows
+// that 16 lanes hold, into row k of the transposed output.
+__device__ __forceinline__ void put_turned(const float (&f)[8], bool pow2, uint8_t *q_t,
+                                           float *scales_t, int64_t k, int64_t m, int64_t M) {
+    float s;
+    const uint2 v = quantize8(f, group_max(f), true, pow2, s);
+    uint8_t *d = q_t + k * M + m;
+    if (m + 8 <= M) {
+        u32x2_any w;
+        w.x = v.x;
+        w.y = v.y;
+        *reinterpret_cast<u32x2_any *>(d) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (m + i < M) d[i] = (uint8_t)((i < 4 ? v.x >> (8 * i) : v.y >> (8 * (i - 4))) & 0xFF);
+    }
+    if ((threadIdx.x & 15) == 0) scales_t[k * ((M + 127) >> 7) + (m >> 7)] = s;
+}
+
+// The gradient for the products that follow: a tile of 128 rows and 128
+// columns (of g and of u).  Rows are quantized as they are loaded; what was
+// loaded goes to LDS as it is, and the tile is read again with a lane holding
+// 8 rows of 4 columns, where the gradient is computed a second time (exact
+// FP32 values of a tile would not fit in LDS twice over, and a rounding of
+// them to fewer bits before the quantizer would be one too many).
+// 16-byte chunk c of row r is at c ^ (r / 8): the 16 lanes that read 8 rows
+// each at one column are on different banks.
+constexpr int kTile = 128;
+constexpr int kTileThreads = 512;
+
+template <class Da, bool kH8>
+struct __align__(16) TurnLds {
+    Da da[kTile][kTile];
+    typename std::conditional<kH8, uint8_t, Bf16>::type g[kTile][kTile], u[kTile][kTile];
+    float sg[kTile], su[kTile];
+};
+
+// Where column c of row r of a tile of T sits: 16-byte chunks of T.
+template <class T>
+__device__ __forceinline__ int tile_at(int r, int c) {
+    constexpr int per = 16 / (int)sizeof(T), chunks = kTile / per;
+    return (((c / per) ^ ((r >> 3) & (chunks - 1))) * per) + c % per;
+}
+
+__device__ __forceinline__ void read4(const Bf16 *p, float (&f)[4]) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
+}
+__device__ __forceinline__ void read4(const float *p, float (&f)[4]) {
+    const float4 v = *reinterpret_cast<const float4 *>(p);
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+}
+__device__ __forceinline__ void read4(const uint8_t *p, float (&f)[4]) {
+    e4m3x4(*reinterpret_cast<const uint32_t *>(p), f);
+}
+
+template <class T>
+__device__ __forceinline__ void write8(T (&row)[kTile], int r, int c, const Raw8<Bf16> &v) {
+    *reinterpret_cast<u32x4 *>(&row[tile_at<T>(r, c)]) = v.v;
+}
+__device__ __forceinline__ void write8(float (&row)[kTile], int r, int c, const Raw8<float> &v) {
+    *reinterpret_cast<u32x4 *>(&row[tile_at<float>(r, c)]) = v.a;
+    *reinterpret_cast<u32x4 *>(&row[tile_at<float>(r, c + 4)]) = v.b;
+}
+__device__ __forceinline__ void write8(uint8_t (&row)[kTile], int r, int c, u32x2_any v) {
+    *reinterpret_cast<uint2 *>(&row[tile_at<uint8_t>(r, c)]) = make_uint2(v.x, v.y);
+}
+
+template <class Da, bool kH8, bool kGelu>
+__global__ __launch_bounds__(kTileThreads) void gated_grad_tile_kernel(GatedGrad p) {
+    __shared__ TurnLds<Da, kH8> L;
+    const int64_t GI = p.I >> 7;
+    const int64_t m0 = (int64_t)blockIdx.x / GI * kTile, gb = (int64_t)blockIdx.x % GI;
+    const int t = threadIdx.x;
+    const int c8 = 8 * (t & 15);
+    const int64_t col = kTile * gb + c8;
+    Raw8<Da> da_raw[4];
+    RawH<kH8> h_raw[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        const int64_t row = m0 + 32 * v + (t >> 4);
+        const int64_t at = row < p.M ? row : p.M - 1;
+        load_raw<false>(static_cast<const Da *>(p.da) + at * p.ld_da + col, 8, da_raw[v]);
+        h_raw[v].load(p, at, col);
+        // rows past the end: da of zero makes all gradients zero but for NaN
+        // and infinity, so g and u are zeros too
+        if (row >= p.M) {
+            zero_raw(da_raw[v]);
+            if constexpr (kH8) {
+                h_raw[v].g.x = h_raw[v].g.y = h_raw[v].u.x = h_raw[v].u.y = 0;
+                h_raw[v].sg = h_raw[v].su = 0.0f;
+            } else {
+                zero_raw(h_raw[v].g);
+                zero_raw(h_raw[v].u);
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        const int r = 32 * v + (t >> 4);
+        const int64_t row = m0 + r;
+        write8(L.da[r], r, c8, da_raw[v]);
+        write8(L.g[r], r, c8, h_raw[v].g);
+        write8(L.u[r], r, c8, h_raw[v].u);
+        if constexpr (kH8) {
+            if (c8 == 0) {
+                L.sg[r] = h_raw[v].sg;
+                L.su[r] = h_raw[v].su;
+            }
+        }
+        if (p.q) {
+            const bool live = row < p.M;
+            float da[8], g[8], u[8], dg[8], du[8];
+            unpack(da_raw[v], da);
+            h_raw[v].get(g, u);
+            grad8<kGelu>(g, u, da, dg, du);
+            put_quantized(dg, live, p.pow2, p.q + row * 2 * p.I + col,
+                          p.scales + row * 2 * GI + gb);
+            put_quantized(du, live, p.pow2, p.q + (row * 2 + 1) * p.I + col,
+                          p.scales + (row * 2 + 1) * GI + gb);
+        }
+    }
+    __syncthreads();
+    if (!p.q_t && !p.a_t) return;
+    const int r0 = 8 * (t & 15), c0 = 4 * (t >> 4);
+    float dg[4][8], du[4][8], a[4][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + i;
+        float da[4], g[4], u[4];
+        read4(&L.da[r][tile_at<Da>(r, c0)], da);
+        read4(&L.g[r][tile_at<typename std::remove_reference<decltype(L.g[0][0])>::type>(r, c0)],
+              g);
+        read4(&L.u[r][tile_at<typename std::remove_reference<decltype(L.u[0][0])>::type>(r, c0)],
+              u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (kH8) {
+                g[j] *= L.sg[r];
+                u[j] *= L.su[r];
+            }
+            gated_grad<kGelu>(g[j], u[j], da[j], dg[j][i], du[j][i], a[j][i]);
+        }
+    }
+    const int64_t k = kTile * gb + c0, m = m0 + r0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (p.q_t) {
+            put_turned(dg[j], p.pow2, p.q_t, p.scales_t, k + j, m, p.M);
+            put_turned(du[j], p.pow2, p.q_t, p.scales_t, p.I + k + j, m, p.M);
+        }
+        if (p.a_t) put_turned(a[j], p.pow2, p.a_t, p.a_scales_t, k + j, m, p.M);
+    }
+}
+
+template <class Da, bool kH8, bool kGelu>
+hipError_t launch_grad(const GatedGrad &p, hipStream_t stream) {
+    const int64_t GI = p.I >> 7;
+    if (p.q_t || p.a_t) {
+        const int64_t tiles = (p.M + kTile - 1) / kTile * GI;
+        hipLaunchKernelGGL((gated_grad_tile_kernel<Da, kH8, kGelu>), dim3((unsigned)tiles),
+                           dim3(kTileThreads), 0, stream, p);
+    } else {
+        const int64_t blocks = (p.M * GI + 15) / 16;
+        hipLaunchKernelGGL((gated_grad_rows_kernel<Da, kH8, kGelu>), dim3((unsigned)blocks),
+                           dim3(256), 0, stream, p);
+    }
+    return hipGetLastError();
+}
+
+template <class Da, bool kH8>
+hipError_t launch_grad(const GatedGrad &p, hipStream_t stream) {
+    return p.gelu ? launch_grad<Da, kH8, true>(p, stream) : launch_grad<Da, kH8, false>(p, stream);
+}
+
+// ---- 8-bit checkpoints ----
+
+// x = code scale: 8 values a thread, a row's last vector its last 8 values.
+template <class T, bool kNarrow>
+__global__ __launch_bounds__(256) void dequant_act_kernel(const uint8_t *__restrict__ q,
+                                                          const float *__restrict__ scales,
+                                                          int64_t M, int64_t K, int64_t vecs,
+                                                          T *__restrict__ x) {
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (id >= M * vecs) return;
+    const int64_t row = id / vecs, v = id % vecs;
+    const Span s = row_span<kNarrow>(v, K);
+    const uint8_t *src = q + row * K + s.col;
+    u32x2_any w;
+    if (!kNarrow) {
+        w = *reinterpret_cast<const u32x2_any *>(src);
+    } else {
+        w.x = w.y = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w.x |= (uint32_t)src[min(i, s.hi - 1)] << (8 * i);
+            w.y |= (uint32_t)src[min(i + 4, s.hi - 1)] << (8 * i);
+        }
+    }
+    // the vector's own values are of one group
+    const float scale = scales[row * ((K + 127) >> 7) + (v >> 4)];
+    float f[8];
+    e4m3x8(w, scale, f);
+    store_span(x + row * K, s, f);
+}
+
+// 1x128 groups (128 columns of a row) to 128x1 groups (128 rows of a column),
+// written transposed: a 128 x 128 tile through LDS, as in the gradient's.
+__global__ __launch_bounds__(kTileThreads) void requant_act_t_kernel(
+    const uint8_t *__restrict__ q, const float *__restrict__ scales, int64_t M, int64_t K,
+    int64_t GK, uint8_t *__restrict__ q_t, float *__restrict__ scales_t, bool pow2) {
+    __shared__ __attribute__((aligned(16))) uint8_t tile[kTile][kTile];
+    __shared__ float ss[kTile];
+    const int64_t m0 = (int64_t)blockIdx.x / GK * kTile, kb = (int64_t)blockIdx.x % GK;
+    const int t = threadIdx.x;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        const int r = 32 * v + (t >> 4), c = 8 * (t & 15);
+        const int64_t row = m0 + r, col = kTile * kb + c;
+        u32x2_any w;
+        w.x = w.y = 0;
+        if (row < M) {
+            const uint8_t *src = q + row * K + col;
+            if (col + 8 <= K) {
+                w = *reinterpret_cast<const u32x2_any *>(src);
+            } else {
+                for (int i = 0; i < 8; ++i)
+                    if (col + i < K) {
+                        if (i < 4)
+                            w.x |= (uint32_t)src[i] << (8 * i);
+                        else
+                            w.y |= (uint32_t)src[i] << (8 * (i - 4));
+                    }
+            }
+        }
+        write8(tile[r], r, c, w);
+        if (c == 0) ss[r] = row < M ? scales[row * GK + kb] : 0.0f;
+    }
+    __syncthreads();
+    const int r0 = 8 * (t & 15), c0 = 4 * (t >> 4);
+    float f[4][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + i;
+        float x[4];
+        read4(&tile[r][tile_at<uint8_t>(r, c0)], x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j][i] = x[j] * ss[r];
+    }
+    const int64_t k = kTile * kb + c0;
+    // 16 lanes share a column: whole groups of lanes leave together
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (k + j < K) put_turned(f[j], pow2, q_t, scales_t, k + j, m0 + r0, M);
+}
+
+}  // namespace
+
+hipError_t launch_gated_grad(const GatedGrad &p, hipStream_t stream) {
+    if (p.da_bf16)
+        return p.h_scales ? launch_grad<Bf16, true>(p, stream) : launch_grad<Bf16, false>(p, stream);
+    return p.h_scales ? launch_grad<float, true>(p, stream) : launch_grad<float, false>(p, stream);
+}
+
+hipError_t launch_dequant_act(const void *q, const float *scales, int64_t M, int64_t K, void *x,
+                              bool bf16_out, hipStream_t stream) {
+    const int64_t vecs = (K + 7) / 8;
+    const dim3 grid((unsigned)((M * vecs + 255) / 256));
+    const uint8_t *src = static_cast<const uint8_t *>(q);
+    auto go = [&](auto kernel, auto *dst) {
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, src, scales, M, K, vecs, dst);
+        return hipGetLastError();
+    };
+    if (bf16_out)
+        return K < 8 ? go(dequant_act_kernel<Bf16, true>, static_cast<Bf16 *>(x))
+                     : go(dequant_act_kernel<Bf16, false>, static_cast<Bf16 *>(x));
+    return K < 8 ? go(dequant_act_kernel<float, true>, static_cast<float *>(x))
+                 : go(dequant_act_kernel<float, false>, static_cast<float *>(x));
+}
+
+hipError_t launch_requant_act_t(const void *q, const float *scales, int64_t M, int64_t K,
+                                void *q_t, float *scales_t, bool pow2, hipStream_t stream) {
+    const int64_t GK = (K + 127) / 128, tiles = (M + kTile - 1) / kTile * GK;
+    hipLaunchKernelGGL(requant_act_t_kernel, dim3((unsigned)tiles), dim3(kTileThreads), 0, stream,
+                       static_cast<const uint8_t *>(q), scales, M, K, GK,
+                       static_cast<uint8_t *>(q_t), scales_t, pow2);
+    return hipGetLastError();
+}
+
+}  // namespace fp8blk
