@@ -42,21 +42,24 @@ __device__ __forceinline__ void grad8(const float (&g)[8], const float (&u)[8],
     }
 }
 
-// g and u of one row's 8 columns as they are stored, and as fp32.
+// g and u of one row's 8 columns as they are stored (u `I` values behind g, its
+// scale `GI` behind g's), and as fp32.
 template <bool kH8>
 struct RawH;
 template <>
 struct RawH<true> {
+    typedef uint8_t Value;
     u32x2_any g, u;
     float sg, su;
-    __device__ __forceinline__ void load(const GatedGrad &p, int64_t row, int64_t col) {
-        const uint8_t *h = static_cast<const uint8_t *>(p.h) + row * p.ld_h + col;
+    __device__ __forceinline__ void load(const uint8_t *h, int64_t I, const float *s, int64_t GI) {
         g = *reinterpret_cast<const u32x2_any *>(h);
-        u = *reinterpret_cast<const u32x2_any *>(h + p.I);
-        const int64_t GI = p.I >> 7;
-        const float *s = p.h_scales + row * 2 * GI + (col >> 7);
+        u = *reinterpret_cast<const u32x2_any *>(h + I);
         sg = s[0];
         su = s[GI];
+    }
+    __device__ __forceinline__ void zero() {
+        g.x = g.y = u.x = u.y = 0;
+        sg = su = 0.0f;
     }
     __device__ __forceinline__ void get(float (&fg)[8], float (&fu)[8]) const {
         e4m3x8(g, sg, fg);
@@ -65,11 +68,15 @@ struct RawH<true> {
 };
 template <>
 struct RawH<false> {
+    typedef Bf16 Value;
     Raw8<Bf16> g, u;
-    __device__ __forceinline__ void load(const GatedGrad &p, int64_t row, int64_t col) {
-        const Bf16 *h = static_cast<const Bf16 *>(p.h) + row * p.ld_h + col;
+    __device__ __forceinline__ void load(const Bf16 *h, int64_t I, const float *, int64_t) {
         load_raw<false>(h, 8, g);
-        load_raw<false>(h + p.I, 8, u);
+        load_raw<false>(h + I, 8, u);
+    }
+    __device__ __forceinline__ void zero() {
+        zero_raw(g);
+        zero_raw(u);
     }
     __device__ __forceinline__ void get(float (&fg)[8], float (&fu)[8]) const {
         unpack(g, fg);
@@ -78,7 +85,7 @@ struct RawH<false> {
 };
 
 // Row by row: 16 lanes to a row's 128 columns, 8 to a lane.
-template <class Da, bool kH8, bool kGelu>
+template <class Da, bool kH8, bool kGelu, bool kPow2>
 __global__ __launch_bounds__(256) void gated_grad_rows_kernel(GatedGrad p) {
     const int64_t GI = p.I >> 7;
     const int64_t id = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
@@ -88,7 +95,8 @@ __global__ __launch_bounds__(256) void gated_grad_rows_kernel(GatedGrad p) {
     Raw8<Da> da_raw;
     RawH<kH8> h_raw;
     load_raw<false>(static_cast<const Da *>(p.da) + row * p.ld_da + col, 8, da_raw);
-    h_raw.load(p, row, col);
+    h_raw.load(static_cast<const typename RawH<kH8>::Value *>(p.h) + row * p.ld_h + col, p.I,
+               p.h_scales + row * 2 * GI + gb, GI);
     float da[8], g[8], u[8], dg[8], du[8];
     unpack(da_raw, da);
     h_raw.get(g, u);
@@ -104,30 +112,31 @@ __global__ __launch_bounds__(256) void gated_grad_rows_kernel(GatedGrad p) {
         }
     }
     if (p.q) {
-        put_quantized(dg, live, p.pow2, p.q + row * 2 * p.I + col, p.scales + row * 2 * GI + gb);
-        put_quantized(du, live, p.pow2, p.q + (row * 2 + 1) * p.I + col,
+        put_quantized(dg, live, kPow2, p.q + row * 2 * p.I + col, p.scales + row * 2 * GI + gb);
+        put_quantized(du, live, kPow2, p.q + (row * 2 + 1) * p.I + col,
                       p.scales + (row * 2 + 1) * GI + gb);
     }
 }
 
-// Eight rows (tokens) m .. m + 7 of one column k, quantized over the 128 rows
-// that 16 lanes hold, into row k of the transposed output.
-__device__ __forceinline__ void put_turned(const float (&f)[8], bool pow2, uint8_t *q_t,
-                                           float *scales_t, int64_t k, int64_t m, int64_t M) {
+// Eight rows (tokens) of one column, quantized over the 128 rows that 16 lanes
+// hold, to `d` of the transposed output (the first `count` of them, which may
+// be none) and the group's scale.
+template <bool kPow2>
+__device__ __forceinline__ void put_turned(const float (&f)[8], uint8_t *d, float *scale,
+                                           int count) {
     float s;
-    const uint2 v = quantize8(f, group_max(f), true, pow2, s);
-    uint8_t *d = q_t + k * M + m;
-    if (m + 8 <= M) {
+    const uint2 v = quantize_group(f, true, kPow2, s);
+    if (count >= 8) {
         u32x2_any w;
         w.x = v.x;
         w.y = v.y;
-        *reinterpret_cast<u32x2_any *>(d) = w;
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x2_any *>(d));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (m + i < M) d[i] = (uint8_t)((i < 4 ? v.x >> (8 * i) : v.y >> (8 * (i - 4))) & 0xFF);
+            if (i < count) d[i] = (uint8_t)((i < 4 ? v.x >> (8 * i) : v.y >> (8 * (i - 4))) & 0xFF);
     }
-    if ((threadIdx.x & 15) == 0) scales_t[k * ((M + 127) >> 7) + (m >> 7)] = s;
+    if ((threadIdx.x & 15) == 0) *scale = s;
 }
 
 // The gradient for the products that follow: a tile of 128 rows and 128
@@ -179,39 +188,45 @@ __device__ __forceinline__ void write8(uint8_t (&row)[kTile], int r, int c, u32x
     *reinterpret_cast<uint2 *>(&row[tile_at<uint8_t>(r, c)]) = make_uint2(v.x, v.y);
 }
 
-template <class Da, bool kH8, bool kGelu>
+template <class Da, bool kH8, bool kGelu, bool kPow2>
 __global__ __launch_bounds__(kTileThreads) void gated_grad_tile_kernel(GatedGrad p) {
     __shared__ TurnLds<Da, kH8> L;
     const int64_t GI = p.I >> 7;
     const int64_t m0 = (int64_t)blockIdx.x / GI * kTile, gb = (int64_t)blockIdx.x % GI;
     const int t = threadIdx.x;
-    const int c8 = 8 * (t & 15);
-    const int64_t col = kTile * gb + c8;
+    const int c8 = 8 * (t & 15), lr = t >> 4;
+    const int64_t row0 = m0 + lr, col = kTile * gb + c8;
+    const int rows = (int)min(p.M - row0, (int64_t)kTile);  // of this thread's, from its first
     Raw8<Da> da_raw[4];
     RawH<kH8> h_raw[4];
+    // addresses go from row to row by sums: products of 64 bits take as long as
+    // a tenth of the rest
+    // (a row past the end is the last one again, and zeroed below)
+    {
+        const int64_t at = min(row0, p.M - 1);
+        const Da *da = static_cast<const Da *>(p.da) + at * p.ld_da + col;
+        const typename RawH<kH8>::Value *h =
+            static_cast<const typename RawH<kH8>::Value *>(p.h) + at * p.ld_h + col;
+        const float *s = p.h_scales + at * 2 * GI + gb;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-        const int64_t row = m0 + 32 * v + (t >> 4);
-        const int64_t at = row < p.M ? row : p.M - 1;
-        load_raw<false>(static_cast<const Da *>(p.da) + at * p.ld_da + col, 8, da_raw[v]);
-        h_raw[v].load(p, at, col);
-        // rows past the end: da of zero makes all gradients zero but for NaN
-        // and infinity, so g and u are zeros too
-        if (row >= p.M) {
-            zero_raw(da_raw[v]);
-            if constexpr (kH8) {
-                h_raw[v].g.x = h_raw[v].g.y = h_raw[v].u.x = h_raw[v].u.y = 0;
-                h_raw[v].sg = h_raw[v].su = 0.0f;
-            } else {
-                zero_raw(h_raw[v].g);
-                zero_raw(h_raw[v].u);
-            }
+        for (int v = 0; v < 4; ++v) {
+            load_raw<false>(da, 8, da_raw[v]);
+            h_raw[v].load(h, p.I, s, GI);
+            const bool next = 32 * (v + 1) < rows;
+            da += next ? 32 * p.ld_da : 0;
+            h += next ? 32 * p.ld_h : 0;
+            s += next ? 64 * GI : 0;
         }
     }
+    uint8_t *q = p.q + row0 * 2 * p.I + col;
+    float *scale = p.scales + row0 * 2 * GI + gb;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-        const int r = 32 * v + (t >> 4);
-        const int64_t row = m0 + r;
+        const int r = 32 * v + lr;
+        if (32 * v >= rows) {  // zeros: their gradient is zero
+            zero_raw(da_raw[v]);
+            h_raw[v].zero();
+        }
         write8(L.da[r], r, c8, da_raw[v]);
         write8(L.g[r], r, c8, h_raw[v].g);
         write8(L.u[r], r, c8, h_raw[v].u);
@@ -222,15 +237,15 @@ __global__ __launch_bounds__(kTileThreads) void gated_grad_tile_kernel(GatedGrad
             }
         }
         if (p.q) {
-            const bool live = row < p.M;
+            const bool live = 32 * v < rows;
             float da[8], g[8], u[8], dg[8], du[8];
             unpack(da_raw[v], da);
             h_raw[v].get(g, u);
             grad8<kGelu>(g, u, da, dg, du);
-            put_quantized(dg, live, p.pow2, p.q + row * 2 * p.I + col,
-                          p.scales + row * 2 * GI + gb);
-            put_quantized(du, live, p.pow2, p.q + (row * 2 + 1) * p.I + col,
-                          p.scales + (row * 2 + 1) * GI + gb);
+            put_quantized(dg, live, kPow2, q, scale);
+            put_quantized(du, live, kPow2, q + p.I, scale + GI);
+            q += 64 * p.I;
+            scale += 64 * GI;
         }
     }
     __syncthreads();
@@ -255,27 +270,30 @@ __global__ __launch_bounds__(kTileThreads) void gated_grad_tile_kernel(GatedGrad
             gated_grad<kGelu>(g[j], u[j], da[j], dg[j][i], du[j][i], a[j][i]);
         }
     }
-    const int64_t k = kTile * gb + c0, m = m0 + r0;
+    const int count = (int)min(p.M - (m0 + r0), (int64_t)8);
+    const int64_t k = kTile * gb + c0, GM = (p.M + 127) >> 7, at = k * p.M + m0 + r0,
+                  group = k * GM + (m0 >> 7), half = p.I * p.M, half_groups = p.I * GM;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+        const int64_t b = at + j * p.M, g = group + j * GM;
         if (p.q_t) {
-            put_turned(dg[j], p.pow2, p.q_t, p.scales_t, k + j, m, p.M);
-            put_turned(du[j], p.pow2, p.q_t, p.scales_t, p.I + k + j, m, p.M);
+            put_turned<kPow2>(dg[j], p.q_t + b, p.scales_t + g, count);
+            put_turned<kPow2>(du[j], p.q_t + half + b, p.scales_t + half_groups + g, count);
         }
-        if (p.a_t) put_turned(a[j], p.pow2, p.a_t, p.a_scales_t, k + j, m, p.M);
+        if (p.a_t) put_turned<kPow2>(a[j], p.a_t + b, p.a_scales_t + g, count);
     }
 }
 
-template <class Da, bool kH8, bool kGelu>
+template <class Da, bool kH8, bool kGelu, bool kPow2>
 hipError_t launch_grad(const GatedGrad &p, hipStream_t stream) {
     const int64_t GI = p.I >> 7;
     if (p.q_t || p.a_t) {
         const int64_t tiles = (p.M + kTile - 1) / kTile * GI;
-        hipLaunchKernelGGL((gated_grad_tile_kernel<Da, kH8, kGelu>), dim3((unsigned)tiles),
+        hipLaunchKernelGGL((gated_grad_tile_kernel<Da, kH8, kGelu, kPow2>), dim3((unsigned)tiles),
                            dim3(kTileThreads), 0, stream, p);
     } else {
         const int64_t blocks = (p.M * GI + 15) / 16;
-        hipLaunchKernelGGL((gated_grad_rows_kernel<Da, kH8, kGelu>), dim3((unsigned)blocks),
+        hipLaunchKernelGGL((gated_grad_rows_kernel<Da, kH8, kGelu, kPow2>), dim3((unsigned)blocks),
                            dim3(256), 0, stream, p);
     }
     return hipGetLastError();
@@ -283,7 +301,11 @@ hipError_t launch_grad(const GatedGrad &p, hipStream_t stream) {
 
 template <class Da, bool kH8>
 hipError_t launch_grad(const GatedGrad &p, hipStream_t stream) {
-    return p.gelu ? launch_grad<Da, kH8, true>(p, stream) : launch_grad<Da, kH8, false>(p, stream);
+    if (p.gelu)
+        return p.pow2 ? launch_grad<Da, kH8, true, true>(p, stream)
+                      : launch_grad<Da, kH8, true, false>(p, stream);
+    return p.pow2 ? launch_grad<Da, kH8, false, true>(p, stream)
+                  : launch_grad<Da, kH8, false, false>(p, stream);
 }
 
 // ---- 8-bit checkpoints ----
@@ -318,53 +340,79 @@ __global__ __launch_bounds__(256) void dequant_act_kernel(const uint8_t *__restr
 }
 
 // 1x128 groups (128 columns of a row) to 128x1 groups (128 rows of a column),
-// written transposed: a 128 x 128 tile through LDS, as in the gradient's.
+// written transposed: 128 x 128 tiles through LDS, as in the gradient's, by
+// workgroups that load the next tile while they work on one.
+constexpr int kTurnGrid = 2 * 256;  // two to a CU (three and four: 10% and 3% slower)
+
+template <bool kPow2>
 __global__ __launch_bounds__(kTileThreads) void requant_act_t_kernel(
     const uint8_t *__restrict__ q, const float *__restrict__ scales, int64_t M, int64_t K,
-    int64_t GK, uint8_t *__restrict__ q_t, float *__restrict__ scales_t, bool pow2) {
+    int64_t GK, int64_t tiles, uint8_t *__restrict__ q_t, float *__restrict__ scales_t) {
     __shared__ __attribute__((aligned(16))) uint8_t tile[kTile][kTile];
     __shared__ float ss[kTile];
-    const int64_t m0 = (int64_t)blockIdx.x / GK * kTile, kb = (int64_t)blockIdx.x % GK;
     const int t = threadIdx.x;
+    const int lr = t >> 4, c = 8 * (t & 15);
+    const int64_t GM = (M + 127) >> 7;
+    u32x2_any raw[4];
+    float scale = 0.0f;
+    auto fetch = [&](int64_t id) {
+        const int64_t m0 = id / GK * kTile, kb = id % GK, col = kTile * kb + c;
+        const int rows = (int)min(M - m0, (int64_t)kTile);
+        const uint8_t *src = q + (m0 + lr) * K + col;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-        const int r = 32 * v + (t >> 4), c = 8 * (t & 15);
-        const int64_t row = m0 + r, col = kTile * kb + c;
-        u32x2_any w;
-        w.x = w.y = 0;
-        if (row < M) {
-            const uint8_t *src = q + row * K + col;
-            if (col + 8 <= K) {
-                w = *reinterpret_cast<const u32x2_any *>(src);
-            } else {
-                for (int i = 0; i < 8; ++i)
-                    if (col + i < K) {
-                        if (i < 4)
-                            w.x |= (uint32_t)src[i] << (8 * i);
-                        else
-                            w.y |= (uint32_t)src[i] << (8 * (i - 4));
-                    }
+        for (int v = 0; v < 4; ++v) {
+            u32x2_any w;
+            w.x = w.y = 0;
+            if (32 * v + lr < rows) {
+                if (col + 8 <= K) {
+                    w = *reinterpret_cast<const u32x2_any *>(src);
+                } else {
+                    for (int i = 0; i < 8; ++i)
+                        if (col + i < K) {
+                            if (i < 4)
+                                w.x |= (uint32_t)src[i] << (8 * i);
+                            else
+                                w.y |= (uint32_t)src[i] << (8 * (i - 4));
+                        }
+                }
             }
+            raw[v] = w;
+            src += 32 * K;
         }
-        write8(tile[r], r, c, w);
-        if (c == 0) ss[r] = row < M ? scales[row * GK + kb] : 0.0f;
+        scale = t < rows ? scales[(m0 + t) * GK + kb] : 0.0f;
+    };
+    int64_t id = blockIdx.x;
+    fetch(id);
+    for (; id < tiles; id += gridDim.x) {
+        const int64_t m0 = id / GK * kTile, kb = id % GK;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) write8(tile[32 * v + lr], 32 * v + lr, c, raw[v]);
+        if (t < kTile) ss[t] = scale;
+        __syncthreads();
+        if (id + gridDim.x < tiles) fetch(id + gridDim.x);
+        const int r0 = 8 * (t & 15), c0 = 4 * (t >> 4);
+        float f[4][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = r0 + i;
+            float x[4];
+            read4(&tile[r][tile_at<uint8_t>(r, c0)], x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j][i] = x[j] * ss[r];
+        }
+        const int64_t k = kTile * kb + c0;
+        const int count = (int)min(M - (m0 + r0), (int64_t)8);
+        uint8_t *d = q_t + k * M + m0 + r0;
+        float *s = scales_t + k * GM + (m0 >> 7);
+        // 16 lanes share a column: whole groups of lanes leave together
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (k + j < K) put_turned<kPow2>(f[j], d, s, count);
+            d += M;
+            s += GM;
+        }
+        __syncthreads();  // the tile's place is the next one's
     }
-    __syncthreads();
-    const int r0 = 8 * (t & 15), c0 = 4 * (t >> 4);
-    float f[4][8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = r0 + i;
-        float x[4];
-        read4(&tile[r][tile_at<uint8_t>(r, c0)], x);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[j][i] = x[j] * ss[r];
-    }
-    const int64_t k = kTile * kb + c0;
-    // 16 lanes share a column: whole groups of lanes leave together
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (k + j < K) put_turned(f[j], pow2, q_t, scales_t, k + j, m0 + r0, M);
 }
 
 }  // namespace
@@ -394,9 +442,15 @@ hipError_t launch_dequant_act(const void *q, const float *scales, int64_t M, int
 hipError_t launch_requant_act_t(const void *q, const float *scales, int64_t M, int64_t K,
                                 void *q_t, float *scales_t, bool pow2, hipStream_t stream) {
     const int64_t GK = (K + 127) / 128, tiles = (M + kTile - 1) / kTile * GK;
-    hipLaunchKernelGGL(requant_act_t_kernel, dim3((unsigned)tiles), dim3(kTileThreads), 0, stream,
-                       static_cast<const uint8_t *>(q), scales, M, K, GK,
-                       static_cast<uint8_t *>(q_t), scales_t, pow2);
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles < kTurnGrid ? tiles : kTurnGrid)),
+                           dim3(kTileThreads), 0, stream, static_cast<const uint8_t *>(q), scales,
+                           M, K, GK, tiles, static_cast<uint8_t *>(q_t), scales_t);
+    };
+    if (pow2)
+        go(requant_act_t_kernel<true>);
+    else
+        go(requant_act_t_kernel<false>);
     return hipGetLastError();
 }
 
