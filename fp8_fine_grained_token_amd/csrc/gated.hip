@@ -23,8 +23,10 @@ namespace {
 
 constexpr int kCUs = 256;
 
-// Fused tiles: 256 x 256 and 128 x 256 (BigTile, MidTile), and 32 x 256 for few
-// rows to a matrix of weights.
+// Fused tiles: 256 x 256 and 128 x 256 (BigTile, MidTile), 64 x 256 where those
+// would leave CUs without work, and 32 x 256 for few rows to a matrix of
+// weights.
+using HalfTile = TileCfg<64, 256, 2, 4, 3>;
 using RowTile = TileCfg<32, 256, 1, 4, 4>;
 // Tiles of a part of the projections (plain products with 2 I columns).
 using PartTile = TileCfg<64, 64, 2, 2, 4>;
@@ -323,25 +325,30 @@ inline int round_up(int x, int m) { return (x + m - 1) / m * m; }
 //     11.7 (9.2 where it needs no second kernel), 16 rows 15.3, against 14.8 and
 //     15.9 for kParts; past 2^24 values of I K or 2048 columns kParts is ahead
 //     (16 rows of 2 x 4096 26 against 18).
-//   kParts: 128 rows of 2 x 1024 19 against 63 fused, 512 rows 32 against 62,
-//     1024 rows 56 against 63, 1536 rows and K 4096 51 against 41: so up to 64
-//     tiles of 128 x 256.  Few rows (32-row tiles): as long as the fused tiles
-//     leave CUs without work.
-// Few rows to a matrix of weights (32 on average at most) run on 32-row tiles
-// with bf16 products, which the weights' copies hide: 128 rows over 32 experts
-// of 2 x 2048 131 us against 148 for 128-row FP8 tiles, 512 rows 178 against
-// 215, 1024 rows 217 against 214.
+//   kParts: 128 rows of 2 x 1024 19 against 46 fused, 512 rows 31 against 46,
+//     640 rows 49 against 52, 1024 rows 54 against 50; with K 2048 512 rows 15.6
+//     against 16.9, 768 rows 21 against 18: so up to 40 tiles of 128 x 256.  Few
+//     rows (32-row tiles): as long as the fused tiles leave CUs without work.
+// Few rows to a matrix of weights (24 on average at most) run on 32-row tiles
+// with bf16 products, which the weights' copies hide: 768 rows over 32 experts
+// of 2 x 2048 177 us against 182 for 64-row FP8 tiles (256 rows 182 against 143,
+// the price of their FP32 sums where a third round of tiles begins); 1024 rows
+// 216 against 182.
+// 64-row FP8 tiles up to 64 rows on average: 1536 such rows 185 against 205 for
+// 128-row tiles, 2048 rows 225 against 211, but 40 against 46 with 2 x 1024 and
+// K 2048.  Dense, where all of them run at once: 1024 rows of 2 x 2048 53
+// against 62, 2048 rows of 2 x 1024 with K 1024 12.6 against 15.6.
 enum Way { kFused, kFew, kParts };
 struct Plan {
     Way way;
     int ksplit, per;  // parts of K, K blocks of a part
 };
-constexpr int64_t kFewTiles = 64;
+constexpr int64_t kFewTiles = 40;
 constexpr int64_t kFewColumns = 8 * kCUs, kFewValues = (int64_t)1 << 24;
-constexpr int64_t kRowsPerMatrix = 32;
+constexpr int64_t kRowTileRows = 24, kHalfTileRows = 64;
 constexpr int64_t kPartExperts = 1024;  // the second kernel's workgroups read all offsets
 
-bool few_rows(int64_t M, int64_t E) { return M <= kRowsPerMatrix * (E ? E : 1); }
+bool few_rows(int64_t M, int64_t E) { return M <= kRowTileRows * (E ? E : 1); }
 // Row tiles of M rows over E experts (0: dense), at most: one more for every
 // expert that has rows.
 int64_t row_tiles(int64_t M, int64_t E, int rows) {
@@ -469,11 +476,14 @@ hipError_t launch_gated_gemm(const GatedGemm &g, hipStream_t stream) {
         p.partial = static_cast<float *>(g.workspace);
         return launch_parts(p, s, stream);
     }
-    if (g.offsets)
-        return few_rows(p.M, p.E) ? launch_grouped_tiles<RowTile, true>(p, stream)
-                                  : launch_grouped_tiles<MidTile, false>(p, stream);
-    const int64_t big = ((p.M + BigTile::BM - 1) / BigTile::BM) * p.tiles_n;
-    if (big >= kCUs) return launch_dense_tiles<BigTile>(p, stream);
+    if (g.offsets) {
+        if (few_rows(p.M, p.E)) return launch_grouped_tiles<RowTile, true>(p, stream);
+        if (p.M <= kHalfTileRows * p.E) return launch_grouped_tiles<HalfTile, false>(p, stream);
+        return launch_grouped_tiles<MidTile, false>(p, stream);
+    }
+    auto tiles = [&](int rows) { return (p.M + rows - 1) / rows * p.tiles_n; };
+    if (tiles(BigTile::BM) >= kCUs) return launch_dense_tiles<BigTile>(p, stream);
+    if (tiles(HalfTile::BM) <= kCUs) return launch_dense_tiles<HalfTile>(p, stream);
     return launch_dense_tiles<MidTile>(p, stream);
 }
 

@@ -68,7 +68,8 @@ def check_act(out, h, act):
 # 4096 fill the card with 256-row tiles, whose last has one row
 SHAPES = [(1, 128, 128), (1, 256, 1152), (3, 384, 128), (16, 128, 7168), (17, 640, 256),
           (64, 256, 640), (127, 128, 1280), (128, 128, 128), (129, 384, 384), (300, 640, 896),
-          (257, 1024, 256), (4097, 2048, 128), (2305, 4096, 384)]
+          (257, 1024, 256), (1000, 2048, 256), (1100, 4096, 128), (4097, 2048, 128),
+          (2305, 4096, 384)]
 
 
 @pytest.mark.parametrize("pow2", [False, True])
@@ -215,7 +216,7 @@ GROUPS = [([1], 0, 128, 128), ([5, 0, 1, 129, 0], 3, 256, 384), ([0, 0, 0], 4, 1
           ([128, 256, 64, 300], 0, 384, 640), ([2] * 70 + [0] * 3, 1, 128, 256),
           ([700, 3, 1], 11, 1024, 256), ([9, 0, 40], 2, 256, 2304),
           ([40, 0, 129, 1, 300], 5, 256, 384), ([64, 64], 0, 128, 1280),
-          ([3] * 40, 2, 2048, 256), ([20, 40, 0, 33, 7, 1, 31, 32], 9, 4096, 128)]
+          ([30, 70, 1, 40], 4, 1408, 256), ([3] * 40, 2, 2048, 256), ([20, 40, 0, 33, 7, 1, 31, 32], 9, 4096, 128)]
 
 
 def sentinels(T, I):
@@ -226,9 +227,9 @@ def sentinels(T, I):
 
 @pytest.mark.parametrize("pow2", [False, True])
 @pytest.mark.parametrize("counts,spare,I,K",
-                         [c for c in GROUPS if sum(c[0]) + c[1] > 32 * len(c[0])])
+                         [c for c in GROUPS if sum(c[0]) + c[1] > 24 * len(c[0])])
 def test_grouped_against_dense(counts, spare, I, K, pow2):
-    # without a workspace (and with more than 32 rows to an expert on average)
+    # without a workspace (and with more than 24 rows to an expert on average)
     # each expert's rows are the dense product, bit for bit; rows behind the last
     # expert's stay as they were
     t = torch()
@@ -310,7 +311,7 @@ def test_grouped_offsets_out_of_order(T, I):
         out = without_workspace("fp8_block_grouped_gemm_gated", a, sa, w, sw, "silu", offsets=off,
                                 outs=t.full((T, I), float("nan"), device="cuda"))
         assert t.equal(t.isnan(out).all(1), ~live) and not t.isnan(out[live]).any()
-        if T > 32 * E:  # FP8 products, the plain call's bit for bit
+        if T > 24 * E:  # FP8 products, the plain call's bit for bit
             check_act(host(out[live]), host(h[live]), "silu")
         split = t.full((T, I), float("nan"), device="cuda")
         F.fp8_block_grouped_gemm_gated(a, sa, w, sw, off, out_dtype="f32", out=split)
