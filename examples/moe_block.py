@@ -6,14 +6,18 @@ Between two attention layers of a decoder, in three forms:
 
   * ``prefill``: many tokens, FP8.  The attention output is normed, gated and
     added to the residual stream, the stream normed again and quantized 1x128
-    in one pass; the quantized rows go to their experts' order, through the
-    grouped FP8 GEMMs, and come back weighted.
+    in one pass; the quantized rows go to their experts' order, through both
+    projections with the activation in one call, whose result is quantized and
+    whose projections are kept in 8 bits, and the second product, and come back
+    weighted.
   * ``decode``: a few tokens, 4-bit weights.  The same with bf16 rows and
     matrix-vector products, which read only the experts that are used.
   * ``backward``: the gradient of ``prefill`` with respect to the attention
     output, the residual stream, the gate, the norms' weights and the routing
     weights (the experts' weights are held fixed, as in fine-tuning around
-    them; their input gradients are FP8 Dgrad products).
+    them; their input gradients are FP8 products with the same weights, the
+    activation's gradient comes quantized from the kept projections).  Nothing
+    in it waits for the GPU.
 
 Each is compared with the same block in fp32 torch on the unquantized weights.
 """
@@ -80,11 +84,12 @@ class MoeBlock:
         weights, ids = self.route(n)
         offsets, slot_row, _ = F.fp8_moe_sort(ids, self.experts)
         xs, xs_scales = F.fp8_moe_dispatch(q, slot_row, scales=scales)
-        h = F.fp8_block_grouped_gemm(xs, xs_scales, self.up_fp8, self.up_scales, offsets)
-        a, a_scales = F.fp8_quant_act_1x128(self.activate(h))
+        a, a_scales, h, h_scales = F.fp8_block_grouped_gemm_gated_quant_1x128(
+            xs, xs_scales, self.up_fp8, self.up_scales, offsets, checkpoint=True)
         ys = F.fp8_block_grouped_gemm(a, a_scales, self.down_fp8, self.down_scales, offsets)
         out = F.fp8_moe_combine(ys, slot_row, weights)
-        return r_out, out, (y, r_out, rstd_post, rstd_pre, weights, offsets, slot_row, h, ys)
+        return r_out, out, (y, r_out, rstd_post, rstd_pre, weights, offsets, slot_row, h,
+                            h_scales, ys)
 
     def decode(self, y, r):
         """The same for a few tokens, on the 4-bit weights."""
@@ -96,28 +101,16 @@ class MoeBlock:
         ys = F.fp8_w4_grouped_matvec(self.activate(h), *self.down_w4, offsets)
         return r_out, F.fp8_moe_combine(ys, slot_row, weights)
 
-    def _dgrad(self, dy, w, scales, offsets):
-        """Input gradient of the experts' products: one Dgrad an expert."""
-        out = torch.empty((dy.shape[0], w.shape[2]), dtype=dy.dtype, device=dy.device)
-        ends = offsets.tolist()
-        for e, (a, b) in enumerate(zip(ends, ends[1:])):
-            if a < b:
-                q, s = F.fp8_quant_act_1x128(dy[a:b])
-                F.fp8_block_gemm_dgrad(q, s, w[e], scales[e], dx=out[a:b])
-        return out
-
     def backward(self, dr_out, dout, saved):
         """Gradients of (y, r, w_post, gate, w_pre, routing weights) from those
         of the new residual stream and of the block output."""
-        y, r_out, rstd_post, rstd_pre, weights, offsets, slot_row, h, ys = saved
+        (y, r_out, rstd_post, rstd_pre, weights, offsets, slot_row, h, h_scales,
+         ys) = saved
         dys, dweights = F.fp8_moe_combine_grad(dout, ys, slot_row, weights)
-        da = self._dgrad(dys, self.down_fp8, self.down_scales, offsets)
-        with torch.enable_grad():
-            leaf = h.detach().float().requires_grad_()
-            half = self.inner
-            act = torch.nn.functional.silu(leaf[:, :half]) * leaf[:, half:]
-        dh, = torch.autograd.grad(act, leaf, da.float())
-        dxs = self._dgrad(dh.to(h.dtype), self.up_fp8, self.up_scales, offsets)
+        da = F.fp8_block_grouped_gemm_dgrad(*F.fp8_quant_act_1x128(dys), self.down_fp8,
+                                            self.down_scales, offsets)
+        dh = F.fp8_gated_grad_quant_1x128(da, h, h_scales)
+        dxs = F.fp8_block_grouped_gemm_dgrad(*dh, self.up_fp8, self.up_scales, offsets)
         dn = F.fp8_moe_dispatch_grad(dxs, slot_row)
         dy, dr, dw_post, dgate, dw_pre = F.fp8_norm_residual_grad(
             dn, dr_out, y, r_out, rstd_post, rstd_pre, self.w_post, self.gate, self.w_pre,

@@ -117,7 +117,8 @@ fp8_status gated_grad(const void *da, int da_dtype, int64_t ld_da, const void *h
     if (M * (I / 128) >= kMaxWorkItems / 16 ||
         (M + 127) / 128 * (I / 128) >= kMaxWorkItems / 512)
         return FP8_ERR_SHAPE;
-    if (quant && ((q != nullptr) != (scales != nullptr) || (q_t != nullptr) != (scales_t != nullptr) ||
+    if (quant && ((q != nullptr) != (scales != nullptr) ||
+                  (q_t != nullptr) != (scales_t != nullptr) ||
                   (a_t != nullptr) != (a_scales_t != nullptr)))
         return FP8_ERR_NULL;
     if (M == 0 || I == 0) return FP8_OK;
@@ -249,20 +250,22 @@ fp8_status fp8_block_grouped_gemm_gated(const void *a_e4m3, const float *a_scale
                                         const void *w_e4m3, const float *w_scales,
                                         const int32_t *group_offsets, int64_t E, int activation,
                                         int64_t T, int64_t I, int64_t K, void *out,
-                                        int out_dtype, void *workspace, size_t workspace_bytes, void *hip_stream) {
+                                        int out_dtype, void *workspace, size_t workspace_bytes,
+                                        void *hip_stream) {
     return gated(a_e4m3, a_scales, w_e4m3, w_scales, {true, group_offsets, E}, activation, T, I, K,
-                 out, out_dtype, nullptr, nullptr, nullptr, nullptr, false, workspace, workspace_bytes, false,
-                 hip_stream);
+                 out, out_dtype, nullptr, nullptr, nullptr, nullptr, false, workspace,
+                 workspace_bytes, false, hip_stream);
 }
 
 fp8_status fp8_block_grouped_gemm_gated_pow2(const void *a_e4m3, const float *a_scales,
                                              const void *w_e4m3, const float *w_scales,
                                              const int32_t *group_offsets, int64_t E,
                                              int activation, int64_t T, int64_t I, int64_t K,
-                                             void *out, int out_dtype, void *workspace, size_t workspace_bytes, void *hip_stream) {
+                                             void *out, int out_dtype, void *workspace,
+                                             size_t workspace_bytes, void *hip_stream) {
     return gated(a_e4m3, a_scales, w_e4m3, w_scales, {true, group_offsets, E}, activation, T, I, K,
-                 out, out_dtype, nullptr, nullptr, nullptr, nullptr, false, workspace, workspace_bytes, true,
-                 hip_stream);
+                 out, out_dtype, nullptr, nullptr, nullptr, nullptr, false, workspace,
+                 workspace_bytes, true, hip_stream);
 }
 
 fp8_status fp8_block_grouped_gemm_gated_quant_1x128(
@@ -271,8 +274,8 @@ fp8_status fp8_block_grouped_gemm_gated_quant_1x128(
     void *q, float *scales, void *h, float *h_scales, void *workspace, size_t workspace_bytes,
     void *hip_stream) {
     return gated(a_e4m3, a_scales, w_e4m3, w_scales, {true, group_offsets, E}, activation, T, I, K,
-                 nullptr, FP8_OUT_BF16, q, scales, h, h_scales, true, workspace, workspace_bytes, false,
-                 hip_stream);
+                 nullptr, FP8_OUT_BF16, q, scales, h, h_scales, true, workspace,
+                 workspace_bytes, false, hip_stream);
 }
 
 fp8_status fp8_block_grouped_gemm_gated_quant_1x128_pow2(
@@ -281,8 +284,8 @@ fp8_status fp8_block_grouped_gemm_gated_quant_1x128_pow2(
     void *q, float *scales, void *h, float *h_scales, void *workspace, size_t workspace_bytes,
     void *hip_stream) {
     return gated(a_e4m3, a_scales, w_e4m3, w_scales, {true, group_offsets, E}, activation, T, I, K,
-                 nullptr, FP8_OUT_BF16, q, scales, h, h_scales, true, workspace, workspace_bytes, true,
-                 hip_stream);
+                 nullptr, FP8_OUT_BF16, q, scales, h, h_scales, true, workspace,
+                 workspace_bytes, true, hip_stream);
 }
 
 fp8_status fp8_gated_grad(const void *da, int da_dtype, int64_t ld_da, const void *h,

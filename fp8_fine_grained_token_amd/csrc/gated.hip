@@ -348,7 +348,7 @@ constexpr int64_t kFewColumns = 8 * kCUs, kFewValues = (int64_t)1 << 24;
 constexpr int64_t kRowTileRows = 24, kHalfTileRows = 64;
 constexpr int64_t kPartExperts = 1024;  // the second kernel's workgroups read all offsets
 
-bool few_rows(int64_t M, int64_t E) { return M <= kRowTileRows * (E ? E : 1); }
+bool few_rows(int64_t M, int64_t E) { return M <= (E ? kRowTileRows * E : RowPartTile::BM); }
 // Row tiles of M rows over E experts (0: dense), at most: one more for every
 // expert that has rows.
 int64_t row_tiles(int64_t M, int64_t E, int rows) {
