@@ -206,7 +206,9 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(const float *__restr
 
 // Grouped GEMM: the tiles are found on the device (find_grouped_tile).
 // kTransW: W [E][K][N] read transposed, the input gradient on the forward
-// weights (see tile_operands_transw).
+// weights (see tile_operands_transw): 8192 rows over 32 experts, 2048 of 7168
+// columns, 205-245 us (1.0-1.2 PFLOP/s), bound as the forward product by the
+// rows that fill up tiles and the last round of them.
 template <class C, int OUT, bool kPow2, bool kTransW = false>
 __global__ __launch_bounds__(C::kThreads) void grouped_gemm_kernel(GemmParams p) {
     __shared__ TileLds<C> lds;

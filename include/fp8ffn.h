@@ -25,9 +25,13 @@
  *   - Tensors are dense and row-major where no row stride (`ld...`, in
  *     elements) is given.
  *   - Outputs and workspaces must not overlap inputs or each other.
- *   - Activations, products and scales are FP32 (sums as in fp8_block_gemm);
- *     an output is rounded to its type once, to nearest even.  Results do not depend on
- *     the run.
+ *   - Activations and scales are FP32; an output is rounded to its type once,
+ *     to nearest even.  Products sum as in fp8_block_gemm or, for few rows, in
+ *     FP32 throughout: which depends on the sizes and on the workspace, never on
+ *     the run, and results do not depend on the run.
+ *   - A workspace is one call's until that call has ended on its stream: calls
+ *     (or replays of captured ones) that may run at the same time take one
+ *     each.
  *   - NaN and infinities: products take finite operands (as fp8_block_gemm);
  *     elsewhere they propagate as the formulas have it, and a group that holds
  *     one is quantized so that it reads back as NaN (its scale is the largest
@@ -98,17 +102,20 @@ size_t fp8_gated_gemm_workspace_bytes(int64_t M, int64_t I, int64_t K);
  * a_e4m3 [T][K] and group_offsets [E+1], clamped as there): w_e4m3 [E][2 I][K],
  * w_scales [E][2 I / 128][K/128]; outputs have T rows, and rows outside every
  * expert's range are left untouched.  E = 0 is refused while T > 0.
+ *   workspace   optional, as above, fp8_grouped_gated_gemm_workspace_bytes()
  */
 fp8_status fp8_block_grouped_gemm_gated(const void *a_e4m3, const float *a_scales,
                                         const void *w_e4m3, const float *w_scales,
                                         const int32_t *group_offsets, int64_t E, int activation,
                                         int64_t T, int64_t I, int64_t K, void *out,
-                                        int out_dtype, void *workspace, size_t workspace_bytes, void *hip_stream);
+                                        int out_dtype, void *workspace,
+                                        size_t workspace_bytes, void *hip_stream);
 fp8_status fp8_block_grouped_gemm_gated_pow2(const void *a_e4m3, const float *a_scales,
                                              const void *w_e4m3, const float *w_scales,
                                              const int32_t *group_offsets, int64_t E,
                                              int activation, int64_t T, int64_t I, int64_t K,
-                                             void *out, int out_dtype, void *workspace, size_t workspace_bytes, void *hip_stream);
+                                             void *out, int out_dtype, void *workspace,
+                                             size_t workspace_bytes, void *hip_stream);
 fp8_status fp8_block_grouped_gemm_gated_quant_1x128(
     const void *a_e4m3, const float *a_scales, const void *w_e4m3, const float *w_scales,
     const int32_t *group_offsets, int64_t E, int activation, int64_t T, int64_t I, int64_t K,
@@ -146,6 +153,9 @@ fp8_status fp8_gated_grad(const void *da, int da_dtype, int64_t ld_da, const voi
  *      weight gradient of W_up (as fp8_quant_act_128x1_t writes them)
  *   a_t [I][M], a_scales_t [I][ceil(M/128)]: a = act(g) u in the same form,
  *      for the weight gradient of W_down
+ * All M rows count.  Rows of h and da that a grouped product left untouched
+ * reach nothing but themselves in q; in q_t and a_t they share a group with
+ * other rows, so they must hold zeros.
  */
 fp8_status fp8_gated_grad_quant(const void *da, int da_dtype, int64_t ld_da, const void *h,
                                 int64_t ld_h, const float *h_scales, int activation, int64_t M,

@@ -222,9 +222,11 @@ for s_ in ("", "_pow2"):
     CALLS["gated" + s_] = (getattr(L, "fp8_block_gemm_gated" + s_), OPERANDS, dict(OUT, **WORK))
     CALLS["gated_quant" + s_] = (kept(getattr(L, "fp8_block_gemm_gated_quant_1x128" + s_)),
                                  OPERANDS, dict(KEPT, **WORK))
-    CALLS["grouped" + s_] = (getattr(L, "fp8_block_grouped_gemm_gated" + s_), GROUPED, dict(OUT, **WORK))
+    CALLS["grouped" + s_] = (getattr(L, "fp8_block_grouped_gemm_gated" + s_), GROUPED,
+                             dict(OUT, **WORK))
     CALLS["grouped_quant" + s_] = (
-        kept(getattr(L, "fp8_block_grouped_gemm_gated_quant_1x128" + s_)), GROUPED, dict(KEPT, **WORK))
+        kept(getattr(L, "fp8_block_grouped_gemm_gated_quant_1x128" + s_)), GROUPED,
+        dict(KEPT, **WORK))
     CALLS["grad_rows" + s_] = (getattr(L, "fp8_gated_grad_quant_1x128" + s_), GRAD, ROWS)
     CALLS["grad_quant" + s_] = (getattr(L, "fp8_gated_grad_quant" + s_), GRAD, TURNED)
     CALLS["requant" + s_] = (getattr(L, "fp8_requant_act_128x1_t" + s_), STORED,

@@ -216,7 +216,8 @@ GROUPS = [([1], 0, 128, 128), ([5, 0, 1, 129, 0], 3, 256, 384), ([0, 0, 0], 4, 1
           ([128, 256, 64, 300], 0, 384, 640), ([2] * 70 + [0] * 3, 1, 128, 256),
           ([700, 3, 1], 11, 1024, 256), ([9, 0, 40], 2, 256, 2304),
           ([40, 0, 129, 1, 300], 5, 256, 384), ([64, 64], 0, 128, 1280),
-          ([30, 70, 1, 40], 4, 1408, 256), ([3] * 40, 2, 2048, 256), ([20, 40, 0, 33, 7, 1, 31, 32], 9, 4096, 128)]
+          ([30, 70, 1, 40], 4, 1408, 256), ([3] * 40, 2, 2048, 256),
+          ([20, 40, 0, 33, 7, 1, 31, 32], 9, 4096, 128)]
 
 
 def sentinels(T, I):
