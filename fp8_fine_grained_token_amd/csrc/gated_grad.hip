@@ -141,26 +141,20 @@ __device__ __forceinline__ void put_turned(const float (&f)[8], uint8_t *d, floa
 }
 
 // The gradient for the products that follow: a tile of 128 rows and 128
-// columns (of g and of u).  Rows are quantized as they are loaded; what was
-// loaded goes to LDS as it is, and the tile is read again with a lane holding
-// 8 rows of 4 columns, where the gradient is computed a second time (exact
-// FP32 values of a tile would not fit in LDS twice over, and a rounding of
-// them to fewer bits before the quantizer would be one too many).
+// columns (of g and of u), computed and quantized 1x128 by rows, 8 columns of
+// four rows to a thread.  For the groups along the other direction a, dg and du
+// go through one FP32 tile in LDS in turn and are read with a lane holding 8
+// rows of 4 columns; dg and du wait in registers (64 values, no more fit beside
+// the loads).
 // 16-byte chunk c of row r is at c ^ (r / 8): the 16 lanes that read 8 rows
 // each at one column are on different banks.
-// 4096 x 2048 from E4M3 with all three outputs: 25-30 us, 2.5-3.1 TB/s.  Bound by
-// vector operations: about 90 for each value of a (two exponentials and
-// reciprocals, five quantized values), and a CU's two tiles load, compute and
-// store nearly in step.  One pass with the values in registers spilled.
+// 4096 x 2048 from E4M3 with all three outputs: 23-28 us, 2.7-3.4 TB/s, from
+// bf16 29 us (3.2).  Bound by vector operations, about 65 for each value of a,
+// which a CU's two tiles run nearly in step with their loads and stores.  With
+// the gradient computed again for the columns, from what was loaded, 93
+// operations: 25-30 us and 35.
 constexpr int kTile = 128;
 constexpr int kTileThreads = 512;
-
-template <class Da, bool kH8>
-struct __align__(16) TurnLds {
-    Da da[kTile][kTile];
-    typename std::conditional<kH8, uint8_t, Bf16>::type g[kTile][kTile], u[kTile][kTile];
-    float sg[kTile], su[kTile];
-};
 
 // Where column c of row r of a tile of T sits: 16-byte chunks of T.
 template <class T>
@@ -169,10 +163,6 @@ __device__ __forceinline__ int tile_at(int r, int c) {
     return (((c / per) ^ ((r >> 3) & (chunks - 1))) * per) + c % per;
 }
 
-__device__ __forceinline__ void read4(const Bf16 *p, float (&f)[4]) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
-}
 __device__ __forceinline__ void read4(const float *p, float (&f)[4]) {
     const float4 v = *reinterpret_cast<const float4 *>(p);
     f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
@@ -181,13 +171,10 @@ __device__ __forceinline__ void read4(const uint8_t *p, float (&f)[4]) {
     e4m3x4(*reinterpret_cast<const uint32_t *>(p), f);
 }
 
-template <class T>
-__device__ __forceinline__ void write8(T (&row)[kTile], int r, int c, const Raw8<Bf16> &v) {
-    *reinterpret_cast<u32x4 *>(&row[tile_at<T>(r, c)]) = v.v;
-}
-__device__ __forceinline__ void write8(float (&row)[kTile], int r, int c, const Raw8<float> &v) {
-    *reinterpret_cast<u32x4 *>(&row[tile_at<float>(r, c)]) = v.a;
-    *reinterpret_cast<u32x4 *>(&row[tile_at<float>(r, c + 4)]) = v.b;
+__device__ __forceinline__ void write8(float (&row)[kTile], int r, int c, const float (&f)[8]) {
+    *reinterpret_cast<float4 *>(&row[tile_at<float>(r, c)]) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4 *>(&row[tile_at<float>(r, c + 4)]) =
+        make_float4(f[4], f[5], f[6], f[7]);
 }
 __device__ __forceinline__ void write8(uint8_t (&row)[kTile], int r, int c, u32x2_any v) {
     *reinterpret_cast<uint2 *>(&row[tile_at<uint8_t>(r, c)]) = make_uint2(v.x, v.y);
@@ -195,7 +182,7 @@ __device__ __forceinline__ void write8(uint8_t (&row)[kTile], int r, int c, u32x
 
 template <class Da, bool kH8, bool kGelu, bool kPow2>
 __global__ __launch_bounds__(kTileThreads) void gated_grad_tile_kernel(GatedGrad p) {
-    __shared__ TurnLds<Da, kH8> L;
+    __shared__ __attribute__((aligned(16))) float tile[kTile][kTile];
     const int64_t GI = p.I >> 7;
     const int64_t m0 = (int64_t)blockIdx.x / GI * kTile, gb = (int64_t)blockIdx.x % GI;
     const int t = threadIdx.x;
@@ -225,68 +212,65 @@ __global__ __launch_bounds__(kTileThreads) void gated_grad_tile_kernel(GatedGrad
     }
     uint8_t *q = p.q + row0 * 2 * p.I + col;
     float *scale = p.scales + row0 * 2 * GI + gb;
+    float dg[4][8], du[4][8];
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
         const int r = 32 * v + lr;
-        if (32 * v >= rows) {  // zeros: their gradient is zero
+        const bool live = 32 * v < rows;
+        if (!live) {  // zeros: their gradient is zero
             zero_raw(da_raw[v]);
             h_raw[v].zero();
         }
-        write8(L.da[r], r, c8, da_raw[v]);
-        write8(L.g[r], r, c8, h_raw[v].g);
-        write8(L.u[r], r, c8, h_raw[v].u);
-        if constexpr (kH8) {
-            if (c8 == 0) {
-                L.sg[r] = h_raw[v].sg;
-                L.su[r] = h_raw[v].su;
-            }
-        }
+        float da[8], g[8], u[8], a[8];
+        unpack(da_raw[v], da);
+        h_raw[v].get(g, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            gated_grad<kGelu>(g[i], u[i], da[i], dg[v][i], du[v][i], a[i]);
+        write8(tile[r], r, c8, a);
         if (p.q) {
-            const bool live = 32 * v < rows;
-            float da[8], g[8], u[8], dg[8], du[8];
-            unpack(da_raw[v], da);
-            h_raw[v].get(g, u);
-            grad8<kGelu>(g, u, da, dg, du);
-            put_quantized(dg, live, kPow2, q, scale);
-            put_quantized(du, live, kPow2, q + p.I, scale + GI);
+            put_quantized(dg[v], live, kPow2, q, scale);
+            put_quantized(du[v], live, kPow2, q + p.I, scale + GI);
             q += 64 * p.I;
             scale += 64 * GI;
         }
     }
-    __syncthreads();
-    if (!p.q_t && !p.a_t) return;
     const int r0 = 8 * (t & 15), c0 = 4 * (t >> 4);
-    float dg[4][8], du[4][8], a[4][8];
+    const int count = (int)min(p.M - (m0 + r0), (int64_t)8);
+    const int64_t GM = (p.M + 127) >> 7;
+    // the tile's columns to rows k, k + 1, .. of a transposed output
+    auto turn = [&](uint8_t *out, float *scales, int64_t k) {
+        float f[4][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = r0 + i;
-        float da[4], g[4], u[4];
-        read4(&L.da[r][tile_at<Da>(r, c0)], da);
-        read4(&L.g[r][tile_at<typename std::remove_reference<decltype(L.g[0][0])>::type>(r, c0)],
-              g);
-        read4(&L.u[r][tile_at<typename std::remove_reference<decltype(L.u[0][0])>::type>(r, c0)],
-              u);
+        for (int i = 0; i < 8; ++i) {
+            float x[4];
+            read4(&tile[r0 + i][tile_at<float>(r0 + i, c0)], x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j][i] = x[j];
+        }
+        uint8_t *d = out + k * p.M + m0 + r0;
+        float *s = scales + k * GM + (m0 >> 7);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if constexpr (kH8) {
-                g[j] *= L.sg[r];
-                u[j] *= L.su[r];
-            }
-            gated_grad<kGelu>(g[j], u[j], da[j], dg[j][i], du[j][i], a[j][i]);
+            put_turned<kPow2>(f[j], d, s, count);
+            d += p.M;
+            s += GM;
         }
-    }
-    const int count = (int)min(p.M - (m0 + r0), (int64_t)8);
-    const int64_t k = kTile * gb + c0, GM = (p.M + 127) >> 7, at = k * p.M + m0 + r0,
-                  group = k * GM + (m0 >> 7), half = p.I * p.M, half_groups = p.I * GM;
+    };
+    auto hold = [&](const float (&f)[4][8]) {
+        __syncthreads();  // the columns before are read
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t b = at + j * p.M, g = group + j * GM;
-        if (p.q_t) {
-            put_turned<kPow2>(dg[j], p.q_t + b, p.scales_t + g, count);
-            put_turned<kPow2>(du[j], p.q_t + half + b, p.scales_t + half_groups + g, count);
-        }
-        if (p.a_t) put_turned<kPow2>(a[j], p.a_t + b, p.a_scales_t + g, count);
-    }
+        for (int v = 0; v < 4; ++v) write8(tile[32 * v + lr], 32 * v + lr, c8, f[v]);
+        __syncthreads();
+    };
+    const int64_t k = kTile * gb + c0;
+    __syncthreads();
+    if (p.a_t) turn(p.a_t, p.a_scales_t, k);
+    if (!p.q_t) return;
+    hold(dg);
+    turn(p.q_t, p.scales_t, k);
+    hold(du);
+    turn(p.q_t, p.scales_t, p.I + k);
 }
 
 template <class Da, bool kH8, bool kGelu, bool kPow2>
