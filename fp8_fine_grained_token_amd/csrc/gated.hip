@@ -341,8 +341,12 @@ inline int round_up(int x, int m) { return (x + m - 1) / m * m; }
 //     (16 rows of 2 x 4096 26 against 18).
 //   kParts: 128 rows of 2 x 1024 19 against 46 fused, 512 rows 31 against 46,
 //     640 rows 49 against 52, 1024 rows 54 against 50; with K 2048 512 rows 15.6
-//     against 16.9, 768 rows 21 against 18: so up to 40 tiles of 128 x 256.  Few
-//     rows (32-row tiles): as long as the fused tiles leave CUs without work.
+//     against 16.9, 768 rows 21 against 18: so up to 40 tiles of 128 x 256.
+//     Per expert, where the fused tiles are less filled, up to 96: 1500 rows over
+//     16 experts of 2 x 256 (56 tiles) 39 against 62, 1000 over 8 of 2 x 384 with
+//     K 2048 (48) 17.6 against 23.7; from 72 to 87 tiles between 6% more and 8%
+//     less time, and FP32 sums.  Few rows (32-row tiles): as long as the fused
+//     tiles leave CUs without work.
 // Few rows to a matrix of weights (24 on average at most) run on 32-row tiles
 // with bf16 products, which the weights' copies hide: 768 rows over 32 experts
 // of 2 x 2048 177 us against 182 for 64-row FP8 tiles (256 rows 182 against 143,
@@ -357,7 +361,7 @@ struct Plan {
     Way way;
     int ksplit, per;  // parts of K, K blocks of a part
 };
-constexpr int64_t kFewTiles = 40;
+constexpr int64_t kFewTiles = 40, kFewGroupedTiles = 96;
 constexpr int64_t kFewColumns = 8 * kCUs, kFewValues = (int64_t)1 << 24;
 constexpr int64_t kRowTileRows = 24, kHalfTileRows = 64;
 constexpr int64_t kPartExperts = 1024;  // the second kernel's workgroups read all offsets
@@ -381,7 +385,8 @@ Plan plan_gated(int64_t M, int64_t E, int64_t I, int64_t K) {
         most = kCUs;
         least = kFewWaves;
     } else if (E <= kPartExperts && (few ? row_tiles(M, E, RowTile::BM) * (I / 128) < kCUs
-                                         : row_tiles(M, E, MidTile::BM) * (I / 128) <= kFewTiles)) {
+                                         : row_tiles(M, E, MidTile::BM) * (I / 128) <=
+                                               (E ? kFewGroupedTiles : kFewTiles))) {
         static_assert(PartTile::BN == RowPartTile::BN, "column tiles");
         tiles = row_tiles(M, E, few ? RowPartTile::BM : PartTile::BM) * (2 * I / PartTile::BN);
     } else {

@@ -21,7 +21,7 @@ DENSE = {"big": (2305, 4096, 384), "mid": (4097, 512, 1152), "half": (1000, 2048
 # rows of each expert, inner width, K: 32-row, 64-row and 128-row tiles, K in
 # parts on 64-row and on 32-row tiles
 GROUPED = {"rows": ([20, 0, 33, 1] * 10, 2048, 1152), "half": ([30, 70, 0, 40] * 4, 2048, 1152),
-           "mid": ([300, 0, 129, 257], 1024, 640), "parts": ([50, 0, 90], 128, 2304),
+           "mid": ([300, 0, 129, 257], 2048, 640), "parts": ([50, 0, 90], 128, 2304),
            "row_parts": ([9, 0, 5], 128, 2304)}
 
 
