@@ -793,10 +793,10 @@ namespace {
 
 // Grouped GEMM over p's operands, W as it is or (kTransW) read transposed, on
 // 128 x 256 tiles.
-template <bool kTransW>
+// `tile`: C's size, for the log.
+template <class C, bool kTransW>
 hipError_t launch_grouped(GemmParams &p, bool bf16_out, bool pow2, const char *entry,
-                          hipStream_t stream) {
-    using C = MidTile;
+                          const char *tile, hipStream_t stream) {
     p.G = (int)(p.K / 128);
     p.NB = (int)(p.N / 128);
     p.tiles_n = (int)((p.N + C::BN - 1) / C::BN);
@@ -805,9 +805,7 @@ hipError_t launch_grouped(GemmParams &p, bool bf16_out, bool pow2, const char *e
     p.ksplit = 1;
     p.kb_per_split = p.G;
     const dim3 grid(round_up(p.ntiles, kNumXcd));
-    log_plan(entry, p.M, p.N, p.K,
-             "128x256 (tiles found on the device; grid sized for the worst case)", 0, 0, 1,
-             (int)grid.x);
+    log_plan(entry, p.M, p.N, p.K, tile, 0, 0, 1, (int)grid.x);
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(C::kThreads), 0, stream, p);
         return hipGetLastError();
@@ -836,12 +834,24 @@ hipError_t launch_grouped_gemm(const void *a, const float *sa, const void *w, co
     p.N = N;
     p.K = K;
     p.E = (int)E;
-    return launch_grouped<false>(p, bf16_out, pow2,
-                                 pow2 ? "block_grouped_gemm_pow2" : "block_grouped_gemm", stream);
+    return launch_grouped<MidTile, false>(
+        p, bf16_out, pow2, pow2 ? "block_grouped_gemm_pow2" : "block_grouped_gemm",
+        "128x256 (tiles found on the device; grid sized for the worst case)", stream);
 }
 
 // Dgrad per expert: dY rows as the activations (inner dimension N), each
 // expert's W read transposed from its forward layout.
+//
+// Tiles (us, against 128 x 256): the smallest that all run at once, 64 x 128
+// (1037 rows over 10 experts, 1024 of 896 columns, 9.8 against 15.9; 1500 over
+// 4, 2048 of 1024, 14.7 against 24.3; in more than a round 1024 over 4, 2048 of
+// 2048, 25.8 against 24.6) or 128 x 128 (the latter 17.9; past a round 4096 over
+// 16, 2048 of 1024, 33 against 26); else 64 x 256 for 64 rows an expert and less
+// (2048 over 32, 4096 of 2048, 77 against 86; 256 over 32 of 7168 166 against
+// 182; 1024 over those 199 against 195).
+using GroupedHalfTile = TileCfg<64, 256, 2, 4, 3>;
+using GroupedShortTile = TileCfg<128, 128, 2, 4, 4>;
+using GroupedSmallTile = TileCfg<64, 128, 2, 4, 4>;
 hipError_t launch_grouped_gemm_dgrad(const void *dy, const float *sdy, const void *w,
                                      const float *sw, const int32_t *offsets, int64_t E,
                                      int64_t T, void *dx, bool bf16_out, int64_t N, int64_t Kx,
@@ -858,9 +868,21 @@ hipError_t launch_grouped_gemm_dgrad(const void *dy, const float *sdy, const voi
     p.K = N;
     p.ldw = Kx;
     p.E = (int)E;
-    return launch_grouped<true>(
-        p, bf16_out, pow2, pow2 ? "block_grouped_gemm_dgrad_pow2" : "block_grouped_gemm_dgrad",
-        stream);
+    const char *entry = pow2 ? "block_grouped_gemm_dgrad_pow2" : "block_grouped_gemm_dgrad";
+    // whether all tiles of this size, at most, run at once
+    auto fit = [&](int rows, int cols) {
+        return ((T + rows - 1) / rows + E) * ((Kx + cols - 1) / cols) <= kCUs;
+    };
+    if (fit(GroupedSmallTile::BM, GroupedSmallTile::BN))
+        return launch_grouped<GroupedSmallTile, true>(p, bf16_out, pow2, entry,
+                                                      "64x128 per expert", stream);
+    if (fit(GroupedShortTile::BM, GroupedShortTile::BN))
+        return launch_grouped<GroupedShortTile, true>(p, bf16_out, pow2, entry,
+                                                      "128x128 per expert", stream);
+    if (T <= 64 * E)
+        return launch_grouped<GroupedHalfTile, true>(p, bf16_out, pow2, entry,
+                                                     "64x256 per expert", stream);
+    return launch_grouped<MidTile, true>(p, bf16_out, pow2, entry, "128x256 per expert", stream);
 }
 
 namespace {

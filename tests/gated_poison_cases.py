@@ -23,6 +23,10 @@ DENSE = {"big": (2305, 4096, 384), "mid": (4097, 512, 1152), "half": (1000, 2048
 GROUPED = {"rows": ([20, 0, 33, 1] * 10, 2048, 1152), "half": ([30, 70, 0, 40] * 4, 2048, 1152),
            "mid": ([300, 0, 129, 257], 2048, 640), "parts": ([50, 0, 90], 128, 2304),
            "row_parts": ([9, 0, 5], 128, 2304)}
+# rows of each expert, inner dimension, columns: 64 x 128, 128 x 128, 64 x 256 and
+# 128 x 256 tiles
+DGRAD = {"small": ([300, 0, 129, 1, 257, 70], 1280, 512), "short": ([300, 200, 1, 500], 1280, 2048),
+         "half": ([20, 0, 65, 7] * 10, 1280, 1152), "mid": ([700, 3, 900], 1280, 4224)}
 
 
 def run_cases():
@@ -61,12 +65,12 @@ def run_cases():
             keep("grouped_" + name + end,
                  *getattr(F, "fp8_block_grouped_gemm_gated_quant_1x128" + end)(
                      *ops, off, checkpoint=True))
-        counts, N, K = [300, 0, 129, 1, 257, 70], 1280, 512
-        dy, s, _, _ = operands(3, sum(counts), 128, N, 0, pow2)
-        _, _, w, sw = operands(4, 1, N // 2, K, len(counts), pow2)
-        off = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).cuda()
-        keep("grouped_dgrad" + end, getattr(F, "fp8_block_grouped_gemm_dgrad" + end)(
-            dy, s, w, sw, off, out_dtype="f32"))
+        for name, (counts, N, K) in DGRAD.items():
+            dy, s, _, _ = operands(3, sum(counts), 128, N, 0, pow2)
+            _, _, w, sw = operands(4, 1, N // 2, K, len(counts), pow2)
+            off = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).cuda()
+            keep("grouped_dgrad_" + name + end, getattr(F, "fp8_block_grouped_gemm_dgrad" + end)(
+                dy, s, w, sw, off, out_dtype="f32"))
     return out
 
 

@@ -330,7 +330,10 @@ def test_grouped_offsets_out_of_order(T, I):
 @pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("counts,spare,N,K", [
     ([1], 0, 128, 128), ([5, 0, 1, 129, 0], 3, 384, 256), ([0, 0], 2, 128, 384),
-    ([128, 256, 64, 300], 0, 640, 384), ([2] * 70, 1, 256, 128), ([700, 3], 11, 1152, 640)])
+    ([128, 256, 64, 300], 0, 640, 384), ([2] * 70, 1, 256, 128), ([700, 3], 11, 1152, 640),
+    # 128 x 128, 64 x 256 and 128 x 256 tiles, the last two with half a column tile
+    ([300, 200, 1, 500], 5, 384, 2048), ([20, 0, 65, 7] * 10, 3, 640, 1152),
+    ([700, 3, 900], 0, 256, 4224)])
 def test_grouped_dgrad_against_dense(counts, spare, N, K, out_dtype, pow2):
     t = torch()
     E, T = len(counts), sum(counts) + spare
