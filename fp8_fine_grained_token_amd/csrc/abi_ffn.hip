@@ -148,7 +148,8 @@ fp8_status gated_grad(const void *da, int da_dtype, int64_t ld_da, const void *h
 
 fp8_status check_stored(const void *q, const float *scales, int64_t M, int64_t K) {
     if (!matrix_ok(M, K)) return FP8_ERR_SHAPE;
-    // one thread to 8 values, or 512 to a tile of 128 rows and columns
+    // one thread to 8 values, or 512 to a tile of 128 rows and columns (which also
+    // keeps a row below 2^30 values: a span's byte offset in it has 32 bits)
     if (M * ((K + 7) / 8) >= kMaxWorkItems - 256 ||
         ((M + 127) / 128) * ((K + 127) / 128) >= kMaxWorkItems / 512)
         return FP8_ERR_SHAPE;

@@ -172,7 +172,9 @@ fp8_status fp8_gated_grad_quant_pow2(const void *da, int da_dtype, int64_t ld_da
 /*
  * 1x128 data read back: x[m][k] = code(q[m][k]) scales[m][k / 128], an FP32
  * product (rounded to bf16 where out_dtype says so).  q [M][K], scales
- * [M][ceil(K/128)], x [M][K]; any M, K and any alignment.
+ * [M][ceil(K/128)], x [M][K]; any alignment, and any M, K with M ceil(K/8)
+ * below 2^32 - 256 and ceil(M/128) ceil(K/128) below 2^23 (FP8_ERR_SHAPE; a
+ * row is so below 2^30 values).
  */
 fp8_status fp8_dequant_act_1x128(const void *q, const float *scales, int64_t M, int64_t K,
                                  void *x, int out_dtype, void *hip_stream);
@@ -181,7 +183,7 @@ fp8_status fp8_dequant_act_1x128(const void *q, const float *scales, int64_t M, 
  * 1x128 data turned for a weight gradient: what fp8_quant_act_128x1_t (or its
  * _pow2 form) gives for the fp32 values that q and scales stand for.
  *   q [M][K], scales [M][ceil(K/128)]; q_t [K][M], scales_t [K][ceil(M/128)]
- * Any M, K.
+ * Any alignment, and M, K as fp8_dequant_act_1x128.
  */
 fp8_status fp8_requant_act_128x1_t(const void *q, const float *scales, int64_t M, int64_t K,
                                    void *q_t, float *scales_t, void *hip_stream);

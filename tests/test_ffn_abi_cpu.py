@@ -175,6 +175,18 @@ def test_checkpoint_errors():
     assert turn(t=N) == B.FP8_ERR_NULL and turn(t=A2) == B.FP8_ERR_ALIGN
 
 
+def test_checkpoint_limits():
+    # M ceil(K/8) below 2^32 - 256, ceil(M/128) ceil(K/128) below 2^23, of which
+    # the second keeps a row's fp32 values below 2^32 bytes
+    for M, K in ((1, 1 << 30), (128, (1 << 30) - 127), (BIG - 1, 9), ((1 << 31) - 128, 16),
+                 (129, 1 << 29)):
+        for name, rest in (("fp8_dequant_act_1x128", (A, F32, N)),
+                           ("fp8_dequant_act_1x128", (A, BF16, N)),
+                           ("fp8_requant_act_128x1_t", (A, A, N)),
+                           ("fp8_requant_act_128x1_t_pow2", (A, A, N))):
+            assert call(name, A, A, M, K, *rest) == B.FP8_ERR_SHAPE, (M, K, name)
+
+
 @pytest.mark.parametrize("suffix", ["", "_pow2"])
 def test_grouped_dgrad_errors(suffix):
     def go(dy=A, sdy=A, w=A, sw=A, off=A, E=3, T=4, dx=A, t=BF16, n=256, k=128):

@@ -50,6 +50,27 @@ def test_checkpoint():
     assert t.equal(q[:, START:], wq) and t.equal(sq[:, START // 128:], ws)
 
 
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+def test_wide_row(out_dtype):
+    # the widest row there may be, whose fp32 values end just below 2^32 bytes,
+    # against the same groups as many short rows
+    t = torch()
+    wide, cut = (1 << 30) - 131, (1 << 30) - (1 << 20)
+    q, s = codes(1, wide), uniform(1, (wide + 127) // 128)
+    x = t.full((1, wide), 7.0, device="cuda").to(t.float32 if out_dtype == "f32" else t.bfloat16)
+    F.fp8_dequant_act_1x128(q, s, out_dtype=out_dtype, x=x)
+    parts = F.fp8_dequant_act_1x128(q[:, :cut].view(-1, 1 << 20),
+                                    s[:, :cut // 128].view(-1, 1 << 13), out_dtype=out_dtype)
+    assert t.equal(x[0, :cut], parts.view(-1))
+    tail = F.fp8_dequant_act_1x128(q[:, cut:].contiguous(), s[:, cut // 128:].contiguous(),
+                                   out_dtype=out_dtype)
+    assert t.equal(x[:, cut:], tail)
+    del x, parts
+    q_t, _ = F.fp8_requant_act_128x1_t(q, s)
+    assert t.equal(q_t[cut:], F.fp8_requant_act_128x1_t(q[:, cut:].contiguous(),
+                                                        s[:, cut // 128:].contiguous())[0])
+
+
 def test_gradient():
     t = torch()
     h, s = codes(M, 2 * I), uniform(M, I // 64) * 2.0 ** -6
