@@ -113,8 +113,9 @@ fp8_status gated_grad(const void *da, int da_dtype, int64_t ld_da, const void *h
         return FP8_ERR_DTYPE;
     if (I < 0 || I >= kMaxDim / 2 || I % 128 != 0 || !matrix_ok(M, 2 * I)) return FP8_ERR_SHAPE;
     if (!stride_ok(M, ld_da) || !stride_ok(M, ld_h)) return FP8_ERR_SHAPE;
-    // 16 threads to a row's 128 columns, or 512 to a tile of 128 rows and columns
-    if (M * (I / 128) >= kMaxWorkItems / 16 ||
+    // 16 threads to a row's 128 columns in workgroups of 256, or 512 to a tile of
+    // 128 rows and columns
+    if (M * (I / 128) > kMaxWorkItems / 16 - 16 ||
         (M + 127) / 128 * (I / 128) >= kMaxWorkItems / 512)
         return FP8_ERR_SHAPE;
     if (quant && ((q != nullptr) != (scales != nullptr) ||

@@ -138,8 +138,8 @@ size_t fp8_grouped_gated_gemm_workspace_bytes(int64_t T, int64_t E, int64_t I, i
  *      [M][2 I / 128] (I % 128 == 0, FP8_ERR_SHAPE), or, where h_scales is
  *      NULL, bf16 (as a plain product wrote it)
  *   dh [M][2 I] of dh_dtype: [dg | du]
- * I % 128 == 0 in all forms.  Pointers need the alignment of one element (q
- * below 8 bytes).
+ * I % 128 == 0 and M I / 128 <= 2^28 - 16 in all forms (FP8_ERR_SHAPE).
+ * Pointers need the alignment of one element (q below 8 bytes).
  */
 fp8_status fp8_gated_grad(const void *da, int da_dtype, int64_t ld_da, const void *h,
                           int64_t ld_h, const float *h_scales, int activation, int64_t M,

@@ -153,6 +153,17 @@ def test_gated_grad_errors():
         assert go(q=A4) == go(s=A2) == go(st=A2) == go(as_=A2) == B.FP8_ERR_ALIGN
 
 
+def test_gated_grad_limit():
+    # 16 threads to a row's 128 columns in workgroups of 256: from M I / 128 =
+    # 2^28 - 15 on the last workgroup is work-item 2^32 (rows may share their
+    # memory: ld 0)
+    for M, I in (((1 << 28) - 1, 128), ((1 << 28) - 15, 128), ((1 << 27) - 7, 256)):
+        for name, rest in (("fp8_gated_grad", (A, BF16)),
+                           ("fp8_gated_grad_quant", (A, A, N, N, N, N)),
+                           ("fp8_gated_grad_quant_pow2", (A, A, A, A, A, A))):
+            assert call(name, A, BF16, 0, A, 0, A, 0, M, I, *rest, N) == B.FP8_ERR_SHAPE, (M, I)
+
+
 def test_checkpoint_errors():
     def read(q=A, s=A, M=4, K=300, x=A, t=BF16):
         return call("fp8_dequant_act_1x128", q, s, M, K, x, t, N)
