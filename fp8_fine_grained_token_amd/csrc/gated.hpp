@@ -43,7 +43,9 @@ __device__ __forceinline__ void gated8(const float (&g)[8], const float (&u)[8],
 
 // Gradients of a = act(g) u at one column: act'(g) = s + g z' s (1 - s) with s
 // = sigmoid(z).  From |g z'| = 128 on s is 0 or 1 and the second term 0, so g z'
-// may stop at any larger value: a finite one, for an infinite g z'.
+// may stop at any larger value: a finite one, for an infinite g z'.  da meets the
+// slope, of magnitude 1.13 at most, before u: da u may overflow where the gate
+// is shut, and infinity times a slope of 0 is NaN.
 constexpr float kFar = 0x1p64f;
 template <bool kGelu>
 __device__ __forceinline__ void gated_grad(float g, float u, float da, float &dg, float &du,
@@ -54,7 +56,7 @@ __device__ __forceinline__ void gated_grad(float g, float u, float da, float &dg
     const float slope = __builtin_fmaf(__builtin_amdgcn_fmed3f(gz, -kFar, kFar), t, s);
     const float act = g * s;
     a = act * u;
-    dg = da * u * slope;
+    dg = da * slope * u;
     du = da * act;
 }
 

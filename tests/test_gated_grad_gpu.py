@@ -129,6 +129,30 @@ def test_kernel_against_differences(act):
     assert (np.abs(dh[:, 128:] - du) <= scale * (1e-8 + 40 * U32)).all()
 
 
+@pytest.mark.parametrize("da_type", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ACTS)
+def test_shut_gates_of_large_products(act, da_type):
+    # da u is past the largest fp32 value, da u act'(g) is not: 0 where the gate
+    # is shut, finite where it nearly is
+    t = torch()
+    I = 128
+    gates = np.array([-300.0, -120.0, -90.0, -20.0, -6.0, -4.5], np.float32)
+    h_np = np.repeat(gates, 2)[:, None].repeat(2 * I, 1)
+    da_np = np.full((12, I), 2.0 ** 64, np.float32)
+    h_np[:, I:] = 2.0 ** 66
+    da_np[1::2] *= -1
+    da = t.from_numpy(da_np).cuda().to(t.bfloat16 if da_type == "bf16" else t.float32)
+    h = t.from_numpy(h_np).cuda().bfloat16()
+    want = da_np.astype(np.float64) * h_np[:, I:] * act64(h_np[:, :I], act)[1]
+    assert np.abs(want).max() < 2.0 ** 127 and np.abs(want).max() > 0
+    dh = F.fp8_gated_grad(da, h, None, act, out_dtype="f32")
+    assert t.isfinite(dh).all()
+    check_grad(host(dh), da_np, h_np, act)
+    for pow2 in ("", "_pow2"):
+        for part in getattr(F, "fp8_gated_grad_quant" + pow2)(da, h, None, act)[1::2]:
+            assert t.isfinite(part).all()
+
+
 @pytest.mark.parametrize("kept", ["e4m3", "bf16"])
 @pytest.mark.parametrize("da_type", ["bf16", "f32"])
 def test_strides_and_alignments(kept, da_type):
