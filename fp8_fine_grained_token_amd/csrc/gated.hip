@@ -120,14 +120,14 @@ __device__ __forceinline__ void gated_tile(const GatedParams &p, TileLds<C> &lds
     gated_store<C>(acc, lds, p.to, row0, row_end, n0);
 }
 
-template <class C, bool kPow2>
+template <class C, bool kPow2, bool kExact = false>
 __global__ __launch_bounds__(C::kThreads) void gated_gemm_kernel(GatedParams p) {
     __shared__ TileLds<C> lds;
     const int t = xcd_logical_tile();
     if (t >= p.ntiles) return;
     int tm, tn;
     raster(t, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
-    gated_tile<C, kPow2, false>(p, lds, p.w, p.sw, (int64_t)tm * C::BM, p.M, (int64_t)tn * 128);
+    gated_tile<C, kPow2, kExact>(p, lds, p.w, p.sw, (int64_t)tm * C::BM, p.M, (int64_t)tn * 128);
 }
 
 // Tiles are found on the device (find_grouped_tile).  128 rows over 32 experts
@@ -356,6 +356,11 @@ inline int round_up(int x, int m) { return (x + m - 1) / m * m; }
 // 128-row tiles, 2048 rows 225 against 211, but 40 against 46 with 2 x 1024 and
 // K 2048.  Dense, where all of them run at once: 1024 rows of 2 x 2048 53
 // against 62, 2048 rows of 2 x 1024 with K 1024 12.6 against 15.6.
+// Dense with a workgroup's 128 columns for every CU (2 x 32768 and wider), where
+// nothing need be split: the tiles of the rows there are.  1 row 76 us on 32-row
+// tiles with bf16 products against 114 on 256-row FP8 ones, 32 rows 81 against
+// 112; 64 rows 83 on 64-row tiles against 116; 128 rows 94 on 128-row tiles
+// against 122.
 enum Way { kFused, kFew, kParts };
 struct Plan {
     Way way;
@@ -442,16 +447,19 @@ hipError_t launch_parts(GatedParams &p, const Plan &s, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <class C>
+template <class C, bool kExact = false>
 hipError_t launch_dense_tiles(GatedParams &p, hipStream_t stream) {
     p.tiles_m = (int)((p.M + C::BM - 1) / C::BM);
     p.ntiles = p.tiles_m * p.tiles_n;
     const dim3 grid(round_up(p.ntiles, kNumXcd));
-    if (p.to.pow2)
-        hipLaunchKernelGGL((gated_gemm_kernel<C, true>), grid, dim3(C::kThreads), 0, stream, p);
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(C::kThreads), 0, stream, p);
+        return hipGetLastError();
+    };
+    if constexpr (kExact)
+        return go(gated_gemm_kernel<C, false, true>);
     else
-        hipLaunchKernelGGL((gated_gemm_kernel<C, false>), grid, dim3(C::kThreads), 0, stream, p);
-    return hipGetLastError();
+        return p.to.pow2 ? go(gated_gemm_kernel<C, true>) : go(gated_gemm_kernel<C, false>);
 }
 
 template <class C, bool kExact>
@@ -500,9 +508,13 @@ hipError_t launch_gated_gemm(const GatedGemm &g, hipStream_t stream) {
         if (p.M <= kHalfTileRows * p.E) return launch_grouped_tiles<HalfTile, false>(p, stream);
         return launch_grouped_tiles<MidTile, false>(p, stream);
     }
+    // (few rows that a workspace would split run on FP8 tiles without one)
+    if (s.way == kFused && few_rows(p.M, 0)) return launch_dense_tiles<RowTile, true>(p, stream);
     auto tiles = [&](int rows) { return (p.M + rows - 1) / rows * p.tiles_n; };
-    if (tiles(BigTile::BM) >= kCUs) return launch_dense_tiles<BigTile>(p, stream);
-    if (tiles(HalfTile::BM) <= kCUs) return launch_dense_tiles<HalfTile>(p, stream);
+    if (p.M <= HalfTile::BM || tiles(HalfTile::BM) <= kCUs)
+        return launch_dense_tiles<HalfTile>(p, stream);
+    if (p.M > MidTile::BM && tiles(BigTile::BM) >= kCUs)
+        return launch_dense_tiles<BigTile>(p, stream);
     return launch_dense_tiles<MidTile>(p, stream);
 }
 

@@ -15,9 +15,10 @@ if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
 # rows, inner width, K: 256-row tiles, 128-row tiles, 64-row tiles, K in parts
-# on 64-row and on 32-row tiles
+# on 64-row and on 32-row tiles, 32-row tiles
 DENSE = {"big": (2305, 4096, 384), "mid": (4097, 512, 1152), "half": (1000, 2048, 1280),
-         "parts": (300, 256, 2304), "row_parts": (30, 128, 2304), "few": (3, 256, 1152)}
+         "parts": (300, 256, 2304), "row_parts": (30, 128, 2304), "few": (3, 256, 1152),
+         "row": (20, 32768, 640)}
 # rows of each expert, inner width, K: 32-row, 64-row and 128-row tiles, K in
 # parts on 64-row and on 32-row tiles
 GROUPED = {"rows": ([20, 0, 33, 1] * 10, 2048, 1152), "half": ([30, 70, 0, 40] * 4, 2048, 1152),

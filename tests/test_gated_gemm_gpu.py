@@ -89,6 +89,22 @@ def test_parts_against_the_plain_product(M, I, K, act, pow2):
     same_quantized(hq, hs, h, pow2, "h")
 
 
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("M", [33, 64, 65, 128, 129])
+def test_many_columns_against_the_plain_product(M, pow2):
+    # 64-row, 128-row and 256-row tiles of one row of tiles
+    I = 32768
+    a, sa, w, sw = operands(M, M, I, 128, pow2)
+    h = host(plain_product(a, sa, w, sw, pow2))
+    name = "fp8_block_gemm_gated"
+    out = without_workspace(name + suffix(pow2), a, sa, w, sw, "silu")
+    check_act(host(out), h, "silu")
+    q, s, hq, hs = without_workspace(name + "_quant_1x128" + suffix(pow2), a, sa, w, sw, "silu",
+                                     quant=True)
+    same_quantized(q, s, host(out), pow2, "a")
+    same_quantized(hq, hs, h, pow2, "h")
+
+
 def exact_product(a, sa, w, sw, rows):
     """[g | u] of some rows in binary64 and the bound on the kernels' fp32."""
     qa, s = a.cpu().numpy(), sa.cpu().numpy()

@@ -105,6 +105,22 @@ def test_dense(M, I, K, act, pow2):
     assert check(out, h, ops, act)
 
 
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("M,K,act", [(1, 256, "silu"), (32, 128, "gelu_tanh")])
+def test_dense_few_rows_of_many_columns(M, K, act, pow2):
+    # enough columns for a workgroup on every CU without parts of K: no workspace,
+    # and none needed for fp32 sums
+    I = 32768
+    ops = outlier_operands(M, M, I, K, pow2)
+    assert L.fp8_gated_gemm_workspace_bytes(M, I, K) == 0
+    name = "fp8_block_gemm_gated"
+    out = getattr(F, name + suffix(pow2))(*ops, act, out_dtype="f32")
+    q, s, _, _ = getattr(F, name + "_quant_1x128" + suffix(pow2))(*ops, act)
+    same_quantized(q, s, host(out), pow2)
+    h = getattr(F, "fp8_block_gemm" + suffix(pow2))(*ops, out_dtype="f32")
+    assert check(out, h, ops, act)
+
+
 # 32-row tiles (24 rows an expert at most), K in parts on 32-row and 64-row tiles
 @pytest.mark.parametrize("pow2", [False, True])
 @pytest.mark.parametrize("counts,I,K,parts", [
