@@ -342,31 +342,45 @@ inline int round_up(int x, int m) { return (x + m - 1) / m * m; }
 //   kParts: 128 rows of 2 x 1024 19 against 46 fused, 512 rows 31 against 46,
 //     640 rows 49 against 52, 1024 rows 54 against 50; with K 2048 512 rows 15.6
 //     against 16.9, 768 rows 21 against 18: so up to 40 tiles of 128 x 256.
-//     Per expert, where the fused tiles are less filled, up to 96: 1500 rows over
-//     16 experts of 2 x 256 (56 tiles) 39 against 62, 1000 over 8 of 2 x 384 with
-//     K 2048 (48) 17.6 against 23.7; from 72 to 87 tiles between 6% more and 8%
-//     less time, and FP32 sums.  Few rows (32-row tiles): as long as the fused
-//     tiles leave CUs without work.
-// Few rows to a matrix of weights (24 on average at most) run on 32-row tiles
-// with bf16 products, which the weights' copies hide: 768 rows over 32 experts
-// of 2 x 2048 177 us against 182 for 64-row FP8 tiles (256 rows 182 against 143,
-// the price of their FP32 sums where a third round of tiles begins); 1024 rows
-// 216 against 182.
+//     Per expert, where the fused tiles are less filled, by the 64 x 64 tiles
+//     there may be.  Up to 576 (two and a quarter a CU, some of them empty): 1000
+//     rows over 8 experts of 2 x 768 (576) 13.0, 24.5, 55 with K 512, 2304, 7168
+//     against 12.7, 26.1, 63; over 4 of 2 x 1024 (640) 17.4, 34.9, 76 against
+//     12.7, 26.2, 63; 1500 over 16 of 2 x 256 39 against 62.  Where 64-row fused
+//     tiles are the others (64 rows on average), up to 288: 500 rows over 16 of
+//     2 x 384 (288) 10.6, 18.6, 38 against 9.5, 20.6, 50; of 2 x 512 (384) 12.2,
+//     22.7, 49 against 9.5, 21.5, 52; short K loses 6 to 13% throughout, for FP32
+//     sums.  Few rows (32-row tiles, the same sums either way), up to 176 tiles of
+//     32 x 256: 16 rows over 8 experts of 2 x 1024 (72) 9.5, 15.3, 31 against 9.4,
+//     20.4, 50; 20 over 32 of 2 x 1024 (168, fewer in use) 10.5, 17.8, 40 against
+//     9.9, 20.4, 51; 150 over 16 of 2 x 1024 (168) 12.3, 24.2, 56 against 10.3,
+//     21.5, 53; 100 over 8 of 2 x 2048 (192) 12.0, 23.1, 55 against 9.8, 21.4, 53,
+//     of 2 x 2560 (240) 13.0, 26.3, 66 against 10.6, 22.8, 56.  Dense up to 128:
+//     17 rows of 2 x 8192 (64) 8.2, 13.9, 26 against 8.4, 19.4, 49, of 2 x 16384
+//     (128) 10.4, 19.0, 47 against 9.4, 20.3, 52, of 2 x 20480 (160) 11.7, 24.3,
+//     60 against 9.7, 21.3, 54.
+// Few rows (24 to an expert's weights on average, 32 to dense ones, which one
+// tile then holds) run on 32-row tiles with bf16 products, which the weights'
+// copies hide: 768 rows over 32 experts of 2 x 2048 177 us against 182 for 64-row
+// FP8 tiles (256 rows 182 against 143, the price of their FP32 sums where a third
+// round of tiles begins); 1024 rows 216 against 182.  Dense parts: 32 rows of 2 x
+// 2048 16.2 against 17.5 on 64-row tiles, 17 to 32 rows of 2 x 128 to 2 x 4096 3
+// to 8% less, 33 to 64 rows between 8% less and 5% more.
 // 64-row FP8 tiles up to 64 rows on average: 1536 such rows 185 against 205 for
 // 128-row tiles, 2048 rows 225 against 211, but 40 against 46 with 2 x 1024 and
 // K 2048.  Dense, where all of them run at once: 1024 rows of 2 x 2048 53
 // against 62, 2048 rows of 2 x 1024 with K 1024 12.6 against 15.6.
-// Dense with a workgroup's 128 columns for every CU (2 x 32768 and wider), where
-// nothing need be split: the tiles of the rows there are.  1 row 76 us on 32-row
-// tiles with bf16 products against 114 on 256-row FP8 ones, 32 rows 81 against
-// 112; 64 rows 83 on 64-row tiles against 116; 128 rows 94 on 128-row tiles
-// against 122.
+// Dense with 128 columns for every CU (2 x 32768 and wider) and at most 128 rows:
+// the tiles of the rows there are.  1 row 76 us on 32-row tiles with bf16
+// products against 114 on 256-row FP8 ones, 32 rows 81 against 112; 64 rows 83 on
+// 64-row tiles against 116; 128 rows 94 on 128-row tiles against 122.
 enum Way { kFused, kFew, kParts };
 struct Plan {
     Way way;
     int ksplit, per;  // parts of K, K blocks of a part
 };
-constexpr int64_t kFewTiles = 40, kFewGroupedTiles = 96;
+constexpr int64_t kFewTiles = 40, kFewPartTiles = 576, kFewPartTilesHalf = 288;
+constexpr int64_t kFewRowTiles = 128, kFewGroupedRowTiles = 176;
 constexpr int64_t kFewColumns = 8 * kCUs, kFewValues = (int64_t)1 << 24;
 constexpr int64_t kRowTileRows = 24, kHalfTileRows = 64;
 constexpr int64_t kPartExperts = 1024;  // the second kernel's workgroups read all offsets
@@ -389,13 +403,15 @@ Plan plan_gated(int64_t M, int64_t E, int64_t I, int64_t K) {
         tiles = I / 8;
         most = kCUs;
         least = kFewWaves;
-    } else if (E <= kPartExperts && (few ? row_tiles(M, E, RowTile::BM) * (I / 128) < kCUs
-                                         : row_tiles(M, E, MidTile::BM) * (I / 128) <=
-                                               (E ? kFewGroupedTiles : kFewTiles))) {
+    } else {
         static_assert(PartTile::BN == RowPartTile::BN, "column tiles");
         tiles = row_tiles(M, E, few ? RowPartTile::BM : PartTile::BM) * (2 * I / PartTile::BN);
-    } else {
-        return {kFused, 1, G};
+        const bool parts =
+            few ? row_tiles(M, E, RowTile::BM) * (I / 128) <=
+                      (E ? kFewGroupedRowTiles : kFewRowTiles)
+            : E ? tiles <= (M <= kHalfTileRows * E ? kFewPartTilesHalf : kFewPartTiles)
+                : row_tiles(M, E, MidTile::BM) * (I / 128) <= kFewTiles;
+        if (!parts || E > kPartExperts) return {kFused, 1, G};
     }
     int s = 1;
     while (tiles * s * 2 <= most && G / (s * 2) >= least) s *= 2;

@@ -121,6 +121,23 @@ def test_workspace_of_sizes_out_of_range():
         assert L.fp8_grouped_gated_gemm_workspace_bytes(4, experts, 128, 128) == 0
 
 
+def test_plans_that_take_a_workspace():
+    # K in parts as long as the 64 x 64 tiles of the parts, at most, are about what
+    # runs at once: with more of them the one-kernel plan is faster
+    need = L.fp8_grouped_gated_gemm_workspace_bytes
+    for K in (512, 2304, 7168):
+        assert need(1000, 8, 768, K) > 0 and need(1000, 4, 768, K) > 0
+        assert need(1000, 4, 1024, K) == need(1600, 16, 512, K) == 0
+        # few rows: 32-row tiles
+        assert L.fp8_gated_gemm_workspace_bytes(17, 16384, K) > 0
+        assert L.fp8_gated_gemm_workspace_bytes(17, 16512, K) == 0
+        assert need(150, 16, 1024, K) > 0 and need(20, 32, 1024, K) > 0
+        assert need(100, 8, 2048, K) == need(500, 32, 512, K) == 0
+        # 64-row tiles as the other plan
+        assert need(500, 16, 384, K) > 0
+        assert need(500, 16, 512, K) == need(1000, 16, 384, K) == need(1600, 64, 128, K) == 0
+
+
 def test_gated_grad_errors():
     def dense(da=A, dt=BF16, ld=256, h=A, ldh=512, hs=A, act=0, M=4, I=256, dh=A, t=BF16):
         return call("fp8_gated_grad", da, dt, ld, h, ldh, hs, act, M, I, dh, t, N)
