@@ -19,6 +19,7 @@
 #include "device_common.hpp"
 #include "gated.hpp"
 #include "gemm_tile.hpp"
+#include "launch.hpp"
 #include "launch_ffn.hpp"
 
 namespace fp8blk {
@@ -425,11 +426,28 @@ size_t plan_bytes(const Plan &s, int64_t M, int64_t I) {
 }
 
 template <class C>
+const char *tile_name() {
+    if (C::BN == PartTile::BN) return C::BM == 64 ? "64x64 parts + sums" : "32x64 parts + sums";
+    return C::BM == 256 ? "256x256" : C::BM == 128 ? "128x256" : C::BM == 64 ? "64x256" : "32x256";
+}
+
+void log_gated(const GatedParams &p, const char *tiles, int ksplit, const dim3 &grid) {
+    static const char *const names[2][2][2] = {
+        {{"block_gemm_gated", "block_gemm_gated_pow2"},
+         {"block_gemm_gated_quant_1x128", "block_gemm_gated_quant_1x128_pow2"}},
+        {{"block_grouped_gemm_gated", "block_grouped_gemm_gated_pow2"},
+         {"block_grouped_gemm_gated_quant_1x128", "block_grouped_gemm_gated_quant_1x128_pow2"}}};
+    log_plan(names[p.offsets != nullptr][p.to.q != nullptr][p.to.pow2], p.M, 2 * p.I, p.K, tiles,
+             0, 0, ksplit, (int)grid.x);
+}
+
+template <class C>
 void launch_part_tiles(GatedParams &p, hipStream_t stream) {
     p.tiles_n = (int)(2 * p.I / C::BN);
     p.tiles_m = (int)row_tiles(p.M, p.E, C::BM);
     p.ntiles = p.tiles_m * p.tiles_n * p.ksplit;
     const dim3 grid(round_up(p.ntiles, kNumXcd));
+    log_gated(p, tile_name<C>(), p.ksplit, grid);
     if (p.offsets)
         hipLaunchKernelGGL((gated_partial_kernel<C, true>), grid, dim3(C::kThreads), 0, stream, p);
     else
@@ -445,8 +463,10 @@ hipError_t launch_parts(GatedParams &p, const Plan &s, hipStream_t stream) {
         p.ntiles = p.tiles_n * p.ksplit;
         // whole sums of the only output need no second kernel
         if (s.ksplit == 1 && !p.to.q) p.partial = nullptr;
-        hipLaunchKernelGGL(gated_few_kernel, dim3(round_up(p.ntiles, kNumXcd)),
-                           dim3(64 * kFewWaves), 0, stream, p);
+        const dim3 grid(round_up(p.ntiles, kNumXcd));
+        log_gated(p, p.partial ? "16x16 in registers + sums" : "16x16 in registers", p.ksplit,
+                  grid);
+        hipLaunchKernelGGL(gated_few_kernel, grid, dim3(64 * kFewWaves), 0, stream, p);
         if (!p.partial) return hipGetLastError();
     } else if (few_rows(p.M, p.E)) {
         launch_part_tiles<RowPartTile>(p, stream);
@@ -468,6 +488,7 @@ hipError_t launch_dense_tiles(GatedParams &p, hipStream_t stream) {
     p.tiles_m = (int)((p.M + C::BM - 1) / C::BM);
     p.ntiles = p.tiles_m * p.tiles_n;
     const dim3 grid(round_up(p.ntiles, kNumXcd));
+    log_gated(p, tile_name<C>(), 1, grid);
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(C::kThreads), 0, stream, p);
         return hipGetLastError();
@@ -482,6 +503,7 @@ template <class C, bool kExact>
 hipError_t launch_grouped_tiles(GatedParams &p, hipStream_t stream) {
     p.tiles_m = (int)row_tiles(p.M, p.E, C::BM);
     const dim3 grid(round_up(p.tiles_m * p.tiles_n, kNumXcd));
+    log_gated(p, tile_name<C>(), 1, grid);
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(C::kThreads), 0, stream, p);
         return hipGetLastError();

@@ -619,6 +619,8 @@ bool plan_log_on() {
     return on;
 }
 
+}  // namespace
+
 void log_plan(const char *entry, int64_t M, int64_t N, int64_t K, const char *tiles, int tn1,
               int tn2, int ksplit, int grid) {
     if (!plan_log_on()) return;
@@ -631,6 +633,8 @@ void log_plan(const char *entry, int64_t M, int64_t N, int64_t K, const char *ti
         fprintf(stderr, "fp8blk: %s M=%lld N=%lld K=%lld tiles=%s ksplit=%d grid=%d\n", entry,
                 (long long)M, (long long)N, (long long)K, tiles, ksplit, grid);
 }
+
+namespace {
 
 // Plan of the dense GEMM family (forward and Dgrad) for the log line.
 void log_dense_plan(const char *entry, const GemmParams &p, const Plan &pl) {
@@ -791,8 +795,7 @@ hipError_t launch_block_gemm_wgrad(const void *a, const float *sa, const void *b
 
 namespace {
 
-// Grouped GEMM over p's operands, W as it is or (kTransW) read transposed, on
-// 128 x 256 tiles.
+// Grouped GEMM over p's operands, W as it is or (kTransW) read transposed.
 // `tile`: C's size, for the log.
 template <class C, bool kTransW>
 hipError_t launch_grouped(GemmParams &p, bool bf16_out, bool pow2, const char *entry,

@@ -7,6 +7,11 @@
 
 namespace fp8blk {
 
+// With FP8BLK_LOG set, one line on stderr for a GEMM about to be launched (tn2 >
+// 0: two kinds of column tiles).
+void log_plan(const char *entry, int64_t M, int64_t N, int64_t K, const char *tiles, int tn1,
+              int tn2, int ksplit, int grid);
+
 // pow2: scales are the smallest powers of two >= amax / 448 (at least
 // 2^-126) instead of amax / 448 itself.
 hipError_t launch_quant_act_1x128(const void *x, int64_t M, int64_t K, void *q, float *scales,
