@@ -62,7 +62,7 @@ MAX_SCLK_MHZ = 2400.0      # the clock that peak is quoted at
 PEAK_HBM_GBS = 8000.0      # MI355X HBM3E
 COUNTERS_FILE = os.path.join(ROOT, "profiles", "counters_dense_gemm.json")
 GEMM_SOURCES = [os.path.join(ROOT, "fp8_fine_grained_token_amd", "csrc", name)
-                for name in ("gemm.hip", "gemm_tile.hpp")]
+                for name in ("gemm.hip", "gemm_tile.hpp", "device_common.hpp")]
 
 M, N, K = 4096, 7168, 7168
 CPU_SAMPLE_ROWS = 512   # ~11 s of oracle work on 16 host threads
