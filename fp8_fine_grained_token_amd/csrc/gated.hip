@@ -351,18 +351,19 @@ inline int round_up(int x, int m) { return (x + m - 1) / m * m; }
 //     rows over 8 experts of 2 x 768 (576) 13.0, 24.5, 55 with K 512, 2304, 7168
 //     against 12.7, 26.1, 63; over 4 of 2 x 1024 (640) 17.4, 34.9, 76 against
 //     12.7, 26.2, 63; 1500 over 16 of 2 x 256 39 against 62.  Where 64-row fused
-//     tiles are the others (64 rows on average), up to 288: 500 rows over 16 of
+//     tiles are the others (64 rows on average), up to 384: 500 rows over 16 of
 //     2 x 384 (288) 10.6, 18.6, 38 against 9.5, 20.6, 50; of 2 x 512 (384) 12.2,
-//     22.7, 49 against 9.5, 21.5, 52; short K loses 6 to 13% throughout, for FP32
-//     sums.  Few rows (32-row tiles, the same sums either way), up to 176 tiles of
-//     32 x 256: 16 rows over 8 experts of 2 x 1024 (72) 9.5, 15.3, 31 against 9.4,
+//     22.7, 49 against 9.5, 21.5, 52; 900 over 32 of 2 x 384 (564) 12.6, 23.5, 54
+//     against 9.8, 21.4, 52.  Short K loses up to a quarter there, for FP32 sums.
+//     Few rows (32-row tiles, the same sums either way), up to 176 tiles of 32 x
+//     256: 16 rows over 8 experts of 2 x 1024 (72) 9.5, 15.3, 31 against 9.4,
 //     20.4, 50; 20 over 32 of 2 x 1024 (168, fewer in use) 10.5, 17.8, 40 against
 //     9.9, 20.4, 51; 150 over 16 of 2 x 1024 (168) 12.3, 24.2, 56 against 10.3,
-//     21.5, 53; 100 over 8 of 2 x 2048 (192) 12.0, 23.1, 55 against 9.8, 21.4, 53,
-//     of 2 x 2560 (240) 13.0, 26.3, 66 against 10.6, 22.8, 56.  Dense up to 128:
-//     17 rows of 2 x 8192 (64) 8.2, 13.9, 26 against 8.4, 19.4, 49, of 2 x 16384
-//     (128) 10.4, 19.0, 47 against 9.4, 20.3, 52, of 2 x 20480 (160) 11.7, 24.3,
-//     60 against 9.7, 21.3, 54.
+//     21.5, 53; 100 over 8 of 2 x 2048 (192) 12.0, 23.1, 55 against 9.8, 21.4,
+//     53, of 2 x 2560 (240) 13.0, 26.3, 66 against 10.6, 22.8, 56.  Dense up to
+//     128: 17 rows of 2 x 8192 (64) 8.2, 13.9, 26 against 8.4, 19.4, 49, of 2 x
+//     16384 (128) 10.4, 19.0, 47 against 9.4, 20.3, 52, of 2 x 20480 (160) 11.7,
+//     24.3, 60 against 9.7, 21.3, 54.
 // Few rows (24 to an expert's weights on average, 32 to dense ones, which one
 // tile then holds) run on 32-row tiles with bf16 products, which the weights'
 // copies hide: 768 rows over 32 experts of 2 x 2048 177 us against 182 for 64-row
@@ -383,7 +384,7 @@ struct Plan {
     Way way;
     int ksplit, per;  // parts of K, K blocks of a part
 };
-constexpr int64_t kFewTiles = 40, kFewPartTiles = 576, kFewPartTilesHalf = 288;
+constexpr int64_t kFewTiles = 40, kFewPartTiles = 576, kFewPartTilesHalf = 384;
 constexpr int64_t kFewRowTiles = 128, kFewGroupedRowTiles = 176;
 constexpr int64_t kFewColumns = 8 * kCUs, kFewValues = (int64_t)1 << 24;
 constexpr int64_t kRowTileRows = 24, kHalfTileRows = 64;
